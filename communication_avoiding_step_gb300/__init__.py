@@ -391,3 +391,11 @@ def train_sharded(data: Dataset, params: Params, w: torch.Tensor, iters: int, ws
                                       _ptr(ws), ws.numel(), _stream(stream), _ptr(xbuf), hook,
                                       None, C.byref(prof)), "casgd_train_sharded")
     return int(prof.launches), int(prof.gram_kind)
+
+
+# ------------------------------------------------------------------------ token models
+from .token_ops import (  # noqa: E402,F401
+    PolicyOut, PreferenceOut, embed, embed_grad, embed_workspace, group_product,
+    group_product_dw, group_product_dx, group_workspace, policy_loss, policy_workspace,
+    preference_loss, preference_workspace,
+)

@@ -29,6 +29,8 @@ FLAG_G_BF16 = 0x2000
 FLAG_GATHER_ROWS = 0x4000
 FLAG_TEST_STALL = 0x80000000
 STAGE_EVENTS = 5
+CASGD_F32, CASGD_BF16, CASGD_F16 = 0, 1, 2
+MAX_GROUPS = 1024
 
 
 class Data(C.Structure):
@@ -49,6 +51,32 @@ class Taps(C.Structure):
 class Profile(C.Structure):
     _fields_ = [("launches", C.c_int64), ("stage_events", C.POINTER(C.c_void_p)),
                 ("n_events", C.c_int32), ("gram_kind", C.c_int32)]
+
+
+class Matrix(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("rows", C.c_int64), ("cols", C.c_int64),
+                ("ld", C.c_int64), ("dtype", C.c_int32)]
+
+
+class Tokens(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("count", C.c_int64), ("wide", C.c_int32)]
+
+
+class Group(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("groups", C.c_int64), ("k", C.c_int64), ("n", C.c_int64),
+                ("dtype", C.c_int32), ("offsets", C.c_void_p), ("x", C.c_void_p),
+                ("ldx", C.c_int64), ("w", C.c_void_p), ("ldw", C.c_int64),
+                ("stride_w", C.c_int64), ("y", C.c_void_p), ("ldy", C.c_int64)]
+
+
+class PreferenceParams(C.Structure):
+    _fields_ = [("beta", C.c_float), ("kind", C.c_int32), ("smoothing", C.c_float),
+                ("mean", C.c_int32), ("grad_scale", C.c_float)]
+
+
+class PolicyParams(C.Structure):
+    _fields_ = [("kl", C.c_float), ("clip_low", C.c_float), ("clip_high", C.c_float),
+                ("temperature", C.c_float), ("grad_scale", C.c_float)]
 
 
 _P = C.POINTER
@@ -98,6 +126,24 @@ SIGNATURES = {
     "casgd_train_sharded": (C.c_int, [_P(Data), _P(Params), C.c_void_p, C.c_uint64, C.c_int32,
                                       C.c_void_p, C.c_size_t, C.c_void_p, C.c_void_p,
                                       ExchangeFn, C.c_void_p, _P(Profile)]),
+    "casgd_embed_workspace_size": (C.c_int, [C.c_int64, C.c_int64, C.c_int64, _P(C.c_size_t)]),
+    "casgd_embed": (C.c_int, [_P(Matrix), _P(Tokens), C.c_float, C.c_int64, _P(Matrix),
+                              C.c_void_p, C.c_size_t, C.c_void_p]),
+    "casgd_embed_grad": (C.c_int, [_P(Matrix), _P(Tokens), C.c_float, C.c_int64, C.c_int32,
+                                   _P(Matrix), C.c_void_p, C.c_size_t, C.c_void_p]),
+    "casgd_group_workspace_size": (C.c_int, [_P(Group), _P(C.c_size_t)]),
+    "casgd_group_product": (C.c_int, [_P(Group), C.c_void_p, C.c_size_t, C.c_void_p]),
+    "casgd_group_product_dx": (C.c_int, [_P(Group), C.c_void_p, C.c_size_t, C.c_void_p]),
+    "casgd_group_product_dw": (C.c_int, [_P(Group), C.c_void_p, C.c_size_t, C.c_void_p]),
+    "casgd_preference_workspace_size": (C.c_int, [C.c_int64, C.c_int64, _P(C.c_size_t)]),
+    "casgd_preference_loss": (C.c_int, [_P(Matrix), _P(Tokens), C.c_void_p, C.c_int64,
+                                        C.c_void_p, _P(PreferenceParams), C.c_void_p,
+                                        C.c_void_p, C.c_void_p, _P(Matrix), C.c_void_p,
+                                        C.c_size_t, C.c_void_p]),
+    "casgd_policy_workspace_size": (C.c_int, [C.c_int64, _P(C.c_size_t)]),
+    "casgd_policy_loss": (C.c_int, [_P(Matrix), _P(Tokens), C.c_void_p, C.c_void_p, C.c_void_p,
+                                    C.c_void_p, _P(PolicyParams), C.c_void_p, C.c_void_p,
+                                    _P(Matrix), C.c_void_p, C.c_size_t, C.c_void_p]),
 }
 
 _lib = None

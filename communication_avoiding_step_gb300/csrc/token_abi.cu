@@ -1,0 +1,201 @@
+// C entry points of the token-model operators (declared in include/casgd.h): argument
+// checks, then the launchers of k_embed.cu, k_group.cu and k_row_loss.cu.
+#include "token_common.cuh"
+
+namespace casgd {
+namespace {
+
+constexpr int64_t kMax31 = int64_t(1) << 31;
+
+bool check_matrix(const casgd_matrix_t* m) {
+  if (!m || m->dtype < CASGD_F32 || m->dtype > CASGD_F16) return false;
+  if (m->rows < 0 || m->rows >= kMax31 || m->cols < 1 || m->cols >= kMax31) return false;
+  if (m->ld < m->cols || m->ld >= kMax31) return false;
+  if (!m->data && m->rows > 0) return false;
+  return reinterpret_cast<uintptr_t>(m->data) % elem_bytes(m->dtype) == 0;
+}
+
+bool check_tokens(const casgd_tokens_t* t) {
+  if (!t || t->count < 0 || t->count >= kMax31 || (t->wide != 0 && t->wide != 1)) return false;
+  if (!t->data && t->count > 0) return false;
+  return reinterpret_cast<uintptr_t>(t->data) % (t->wide ? 8 : 4) == 0;
+}
+
+bool aligned4(const void* p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
+
+Mat mat(const casgd_matrix_t* m) { return {m->data, m->rows, m->cols, m->ld, m->dtype}; }
+
+int check_ws(const void* ws, size_t have, size_t need) {
+  if (!ws || reinterpret_cast<uintptr_t>(ws) % 256 != 0 || have < need) return CASGD_ERR_WORKSPACE;
+  return CASGD_OK;
+}
+
+// A context whose launches may be scheduled while the one before them in the stream ends
+// (every kernel here waits for it before it touches memory).
+int make_ctx(void* stream, Ctx& c) {
+  c = Ctx{static_cast<cudaStream_t>(stream), 0, 0};
+  c.pdl = true;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&c.num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return CASGD_ERR_CUDA;
+  return CASGD_OK;
+}
+
+int done(cudaError_t e) { return e == cudaSuccess ? CASGD_OK : CASGD_ERR_CUDA; }
+
+bool check_group(const casgd_group_t* g) {
+  if (!g || (g->dtype != CASGD_BF16 && g->dtype != CASGD_F16)) return false;
+  if (g->rows < 0 || g->rows >= kMax31 || g->groups < 1 || g->groups > CASGD_MAX_GROUPS)
+    return false;
+  if (g->k < 1 || g->n < 1 || g->k >= kMax31 || g->n >= kMax31) return false;
+  if (g->ldx < g->k || g->ldw < g->k || g->ldy < g->n) return false;
+  if (g->ldx >= kMax31 || g->ldw >= kMax31 || g->ldy >= kMax31) return false;
+  return g->groups == 1 || (g->stride_w >= (g->n - 1) * g->ldw + g->k &&
+                            g->stride_w < (int64_t(1) << 40));
+}
+
+GroupArgs group_args(const casgd_group_t* g) {
+  return {g->rows, g->groups, g->k, g->n, g->dtype, g->offsets, g->x, g->ldx, g->w, g->ldw,
+          g->stride_w, g->y, g->ldy};
+}
+
+int group_call(GroupDir dir, const casgd_group_t* g, void* ws, size_t ws_bytes, void* stream) {
+  if (!check_group(g) || !g->offsets || !aligned4(g->offsets) || !g->w) return CASGD_ERR_ARG;
+  if (g->rows > 0 && (!g->x || !g->y)) return CASGD_ERR_ARG;
+  if ((reinterpret_cast<uintptr_t>(g->x) | reinterpret_cast<uintptr_t>(g->w) |
+       reinterpret_cast<uintptr_t>(g->y)) % 2 != 0)
+    return CASGD_ERR_ARG;
+  size_t need = 0;
+  int rc = casgd_group_workspace_size(g, &need);
+  if (rc == CASGD_OK) rc = check_ws(ws, ws_bytes, need);
+  if (rc != CASGD_OK) return rc;
+  Ctx c{};
+  if ((rc = make_ctx(stream, c)) != CASGD_OK) return rc;
+  return done(launch_group(dir, group_args(g), static_cast<Ctrl*>(ws), c));
+}
+
+// Logits, targets and an optional gradient of the logits' shape and type.
+bool check_rows(const casgd_matrix_t* x, const casgd_tokens_t* t, const casgd_matrix_t* g) {
+  if (!check_matrix(x) || !check_tokens(t) || t->count != x->rows) return false;
+  if (!g) return true;
+  if (!check_matrix(g) || g->rows != x->rows || g->cols != x->cols || g->dtype != x->dtype)
+    return false;
+  return g->data != x->data || g->ld == x->ld;
+}
+
+}  // namespace
+}  // namespace casgd
+
+using namespace casgd;
+
+extern "C" {
+
+int casgd_embed_workspace_size(int64_t rows, int64_t vocab, int64_t dim, size_t* bytes) {
+  if (!bytes || rows < 0 || vocab < 1 || dim < 1 || rows >= kMax31 || vocab >= kMax31 ||
+      dim >= kMax31)
+    return CASGD_ERR_ARG;
+  *bytes = embed_workspace_bytes(rows, vocab, dim);
+  return CASGD_OK;
+}
+
+int casgd_embed(const casgd_matrix_t* table, const casgd_tokens_t* tokens, float scale,
+                int64_t padding_id, const casgd_matrix_t* out, void* ws, size_t ws_bytes,
+                void* stream) {
+  if (!check_matrix(table) || table->rows < 1 || !check_tokens(tokens) || !check_matrix(out) ||
+      out->rows != tokens->count || out->cols != table->cols)
+    return CASGD_ERR_ARG;
+  int rc = check_ws(ws, ws_bytes, sizeof(Ctrl));
+  Ctx c{};
+  if (rc != CASGD_OK || (rc = make_ctx(stream, c)) != CASGD_OK) return rc;
+  return done(launch_embed(mat(table), {tokens->data, tokens->wide}, scale, padding_id, mat(out),
+                           static_cast<Ctrl*>(ws), c));
+}
+
+int casgd_embed_grad(const casgd_matrix_t* dout, const casgd_tokens_t* tokens, float scale,
+                     int64_t padding_id, int32_t accumulate, const casgd_matrix_t* grad,
+                     void* ws, size_t ws_bytes, void* stream) {
+  if (!check_matrix(dout) || !check_tokens(tokens) || !check_matrix(grad) || grad->rows < 1 ||
+      dout->rows != tokens->count || dout->cols != grad->cols ||
+      (accumulate != 0 && accumulate != 1))
+    return CASGD_ERR_ARG;
+  int rc = check_ws(ws, ws_bytes, embed_workspace_bytes(dout->rows, grad->rows, dout->cols));
+  Ctx c{};
+  if (rc != CASGD_OK || (rc = make_ctx(stream, c)) != CASGD_OK) return rc;
+  return done(launch_embed_grad(mat(dout), {tokens->data, tokens->wide}, scale, padding_id,
+                                accumulate != 0, mat(grad), ws, c));
+}
+
+int casgd_group_workspace_size(const casgd_group_t* g, size_t* bytes) {
+  if (!bytes || !check_group(g)) return CASGD_ERR_ARG;
+  *bytes = 512;
+  return CASGD_OK;
+}
+
+int casgd_group_product(const casgd_group_t* g, void* ws, size_t ws_bytes, void* stream) {
+  return group_call(GROUP_Y, g, ws, ws_bytes, stream);
+}
+int casgd_group_product_dx(const casgd_group_t* g, void* ws, size_t ws_bytes, void* stream) {
+  return group_call(GROUP_DX, g, ws, ws_bytes, stream);
+}
+int casgd_group_product_dw(const casgd_group_t* g, void* ws, size_t ws_bytes, void* stream) {
+  return group_call(GROUP_DW, g, ws, ws_bytes, stream);
+}
+
+int casgd_preference_workspace_size(int64_t rows, int64_t pairs, size_t* bytes) {
+  if (!bytes || rows < 0 || rows >= kMax31 || pairs < 1 || pairs >= kMax31 / 2)
+    return CASGD_ERR_ARG;
+  *bytes = preference_workspace_bytes(rows, pairs);
+  return CASGD_OK;
+}
+
+int casgd_preference_loss(const casgd_matrix_t* logits, const casgd_tokens_t* targets,
+                          const int32_t* seq_offsets, int64_t pairs, const float* ref_logp,
+                          const casgd_preference_t* p, float* loss, float* margin, float* logp,
+                          const casgd_matrix_t* grad, void* ws, size_t ws_bytes, void* stream) {
+  if (!check_rows(logits, targets, grad) || pairs < 1 || pairs >= kMax31 / 2 || !p)
+    return CASGD_ERR_ARG;
+  if (!seq_offsets || !ref_logp || !loss || !margin || !logp || !aligned4(seq_offsets) ||
+      !aligned4(ref_logp) || !aligned4(loss) || !aligned4(margin) || !aligned4(logp))
+    return CASGD_ERR_ARG;
+  if (p->kind != CASGD_LOGISTIC && p->kind != CASGD_LSQ) return CASGD_ERR_ARG;
+  if (!(p->beta == p->beta) || !(p->smoothing >= 0.0f && p->smoothing <= 1.0f) ||
+      (p->mean != 0 && p->mean != 1) || !(p->grad_scale == p->grad_scale))
+    return CASGD_ERR_ARG;
+  int rc = check_ws(ws, ws_bytes, preference_workspace_bytes(logits->rows, pairs));
+  Ctx c{};
+  if (rc != CASGD_OK || (rc = make_ctx(stream, c)) != CASGD_OK) return rc;
+  PrefArgs a{mat(logits), grad ? mat(grad) : Mat{}, {targets->data, targets->wide}, seq_offsets,
+             pairs, ref_logp, p->beta, p->smoothing, p->grad_scale, p->kind, p->mean, loss,
+             margin, logp};
+  return done(launch_preference(a, ws, c));
+}
+
+int casgd_policy_workspace_size(int64_t rows, size_t* bytes) {
+  if (!bytes || rows < 0 || rows >= kMax31) return CASGD_ERR_ARG;
+  *bytes = policy_workspace_bytes(rows);
+  return CASGD_OK;
+}
+
+int casgd_policy_loss(const casgd_matrix_t* logits, const casgd_tokens_t* targets,
+                      const float* weights, const float* old_logp, const float* ref_logp,
+                      const float* adv, const casgd_policy_t* p, float* stats, float* logp,
+                      const casgd_matrix_t* grad, void* ws, size_t ws_bytes, void* stream) {
+  if (!check_rows(logits, targets, grad) || !p || !stats || !aligned4(stats)) return CASGD_ERR_ARG;
+  if (logits->rows > 0 && (!weights || !old_logp || !adv || !logp)) return CASGD_ERR_ARG;
+  if (!aligned4(weights) || !aligned4(old_logp) || !aligned4(ref_logp) || !aligned4(adv) ||
+      !aligned4(logp))
+    return CASGD_ERR_ARG;
+  if (!(p->kl == p->kl) || !(p->clip_low >= 0.0f) || !(p->clip_high >= 0.0f) ||
+      !(p->temperature > 0.0f) || !(p->grad_scale == p->grad_scale))
+    return CASGD_ERR_ARG;
+  int rc = check_ws(ws, ws_bytes, policy_workspace_bytes(logits->rows));
+  Ctx c{};
+  if (rc != CASGD_OK || (rc = make_ctx(stream, c)) != CASGD_OK) return rc;
+  PolicyArgs a{mat(logits), grad ? mat(grad) : Mat{}, {targets->data, targets->wide}, weights,
+               old_logp, ref_logp, adv, p->kl, p->clip_low, p->clip_high, p->temperature,
+               p->grad_scale, stats, logp};
+  return done(launch_policy(a, ws, c));
+}
+
+}  // extern "C"

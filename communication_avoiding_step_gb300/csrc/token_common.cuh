@@ -1,0 +1,111 @@
+// Shared pieces of the token-model operators (embedding lookup, products grouped by
+// expert, preference and policy losses): element types, token numbers, reductions and
+// the launchers called by token_abi.cu.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "casgd_internal.cuh"
+
+namespace casgd {
+
+// Element types, as CASGD_F32 / CASGD_BF16 / CASGD_F16 name them.
+template <class T>
+struct Elem;
+template <>
+struct Elem<float> {
+  static __device__ __forceinline__ float get(float v) { return v; }
+  static __device__ __forceinline__ float put(float v) { return v; }
+};
+template <>
+struct Elem<__nv_bfloat16> {
+  static __device__ __forceinline__ float get(__nv_bfloat16 v) { return __bfloat162float(v); }
+  static __device__ __forceinline__ __nv_bfloat16 put(float v) { return __float2bfloat16_rn(v); }
+};
+template <>
+struct Elem<__half> {
+  static __device__ __forceinline__ float get(__half v) { return __half2float(v); }
+  static __device__ __forceinline__ __half put(float v) { return __float2half_rn(v); }
+};
+
+// N consecutive elements as one aligned access of N * sizeof(T) bytes.
+template <class T, int N>
+struct alignas(N * sizeof(T)) Pack {
+  T v[N];
+};
+
+inline int64_t elem_bytes(int32_t dtype) { return dtype == CASGD_F32 ? 4 : 2; }
+
+// Token number i of an int32 or int64 array.
+struct Ids {
+  const void* p;
+  int wide;
+  __device__ __forceinline__ int64_t at(int64_t i) const {
+    return wide ? static_cast<const int64_t*>(p)[i]
+                : (int64_t) static_cast<const int32_t*>(p)[i];
+  }
+};
+
+struct Mat {  // row-major device matrix, ld elements from row to row
+  void* p;
+  int64_t rows, cols, ld;
+  int32_t dtype;
+};
+
+// Whether every row of the matrix starts on a multiple of `bytes`, and rows are whole
+// multiples of it.
+inline bool rows_aligned(const Mat& m, int64_t bytes) {
+  const int64_t es = elem_bytes(m.dtype);
+  return reinterpret_cast<uintptr_t>(m.p) % bytes == 0 && (m.ld * es) % bytes == 0 &&
+         (m.cols * es) % bytes == 0;
+}
+
+__device__ __forceinline__ void set_status(Ctrl* c, uint32_t bit) { atomicOr(&c->status, bit); }
+
+// ------------------------------------------------------------------ embedding (k_embed.cu)
+size_t embed_workspace_bytes(int64_t rows, int64_t vocab, int64_t dim);
+cudaError_t launch_embed(const Mat& table, Ids ids, float scale, int64_t padding_id,
+                         const Mat& out, Ctrl* ctrl, Ctx& c);
+cudaError_t launch_embed_grad(const Mat& dout, Ids ids, float scale, int64_t padding_id,
+                              bool accumulate, const Mat& grad, void* ws, Ctx& c);
+
+// ------------------------------------------------------------------ experts (k_group.cu)
+enum GroupDir { GROUP_Y = 0, GROUP_DX = 1, GROUP_DW = 2 };
+struct GroupArgs {
+  int64_t rows, groups, k, n;
+  int32_t dtype;
+  const int32_t* offsets;
+  void* x;   // rows x k
+  int64_t ldx;
+  void* w;   // groups x n x k
+  int64_t ldw, stride_w;
+  void* y;   // rows x n
+  int64_t ldy;
+};
+cudaError_t launch_group(GroupDir dir, const GroupArgs& g, Ctrl* ctrl, Ctx& c);
+
+// ------------------------------------------------------------------ losses (k_row_loss.cu)
+struct PrefArgs {
+  Mat logits, grad;  // grad.p null: none
+  Ids targets;
+  const int32_t* offsets;
+  int64_t pairs;
+  const float* ref;
+  float beta, smoothing, grad_scale;
+  int kind, mean;
+  float *loss, *margin, *logp;
+};
+struct PolicyArgs {
+  Mat logits, grad;
+  Ids targets;
+  const float *weights, *old_logp, *ref_logp, *adv;  // ref_logp null: no KL term
+  float kl, clip_low, clip_high, temperature, grad_scale;
+  float *stats, *logp;
+};
+size_t preference_workspace_bytes(int64_t rows, int64_t pairs);
+size_t policy_workspace_bytes(int64_t rows);
+cudaError_t launch_preference(const PrefArgs& p, void* ws, Ctx& c);
+cudaError_t launch_policy(const PolicyArgs& p, void* ws, Ctx& c);
+
+}  // namespace casgd

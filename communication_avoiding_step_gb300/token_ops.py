@@ -1,0 +1,267 @@
+"""Token-model operators on PyTorch tensors: embedding lookup and its gradient, matrix
+products grouped by expert, the preference loss and the clipped policy loss with their
+gradients.  Like the rest of the binding this module only marshals tensors into the C ABI
+of include/casgd.h, where each call's mathematics and limits are stated.
+
+Every call takes its outputs and a workspace from the caller, allocates nothing and is
+asynchronous on `stream` (default: the current stream).  A workspace serves one stream at
+a time.  Tensors that were made or used on another stream have to be ordered before the
+call, and kept alive until it is done, as with any call that takes a stream.
+"""
+from __future__ import annotations
+
+import ctypes as C
+from dataclasses import dataclass
+
+import torch
+
+from ._native import (
+    CASGD_BF16, CASGD_F16, CASGD_F32, CASGD_LOGISTIC, MAX_GROUPS, Group, Matrix,
+    PolicyParams, PreferenceParams, Tokens, check as _check, load,
+)
+
+_DTYPES = {torch.float32: CASGD_F32, torch.bfloat16: CASGD_BF16, torch.float16: CASGD_F16}
+
+
+def _stream(stream) -> C.c_void_p:
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    return C.c_void_p(stream.cuda_stream)
+
+
+def _matrix(t: torch.Tensor, name: str) -> Matrix:
+    """A 2-D CUDA tensor whose rows are contiguous (any row stride of at least its width)."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor")
+    dtype = _DTYPES.get(t.dtype)
+    if dtype is None:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    rows, cols = t.shape
+    ld, inner = t.stride()
+    if cols < 1:
+        raise ValueError(f"{name} must have at least one column")
+    if rows <= 1:
+        ld = max(ld, cols)
+    if (inner != 1 and cols > 1) or ld < cols:
+        raise ValueError(f"{name} must have contiguous, non-overlapping rows")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return Matrix(t.data_ptr(), rows, cols, ld, dtype)
+
+
+def _tokens(t: torch.Tensor, name: str) -> Tokens:
+    if not isinstance(t, torch.Tensor) or t.dtype not in (torch.int64, torch.int32):
+        raise ValueError(f"{name} must be an int32 or int64 tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return Tokens(t.data_ptr(), t.numel(), 1 if t.dtype == torch.int64 else 0)
+
+
+def _vector(t: torch.Tensor, name: str, dtype, numel: int) -> C.c_void_p:
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.numel() < numel:
+        raise ValueError(f"{name} must be a {dtype} tensor of at least {numel} elements")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return C.c_void_p(t.data_ptr())
+
+
+def _workspace(size_call: str, *args, device="cuda", stream=None) -> torch.Tensor:
+    nbytes = C.c_size_t(0)
+    _check(getattr(load(), size_call)(*args, C.byref(nbytes)), size_call)
+    ws = torch.empty(nbytes.value, dtype=torch.uint8, device=device)
+    _check(load().casgd_workspace_init(C.c_void_p(ws.data_ptr()), ws.numel(), _stream(stream)),
+           "casgd_workspace_init")
+    return ws
+
+
+def _ws(ws: torch.Tensor) -> tuple:
+    if not isinstance(ws, torch.Tensor) or not ws.is_cuda or ws.dtype != torch.uint8 \
+            or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous uint8 CUDA tensor (see the *_workspace calls)")
+    return C.c_void_p(ws.data_ptr()), ws.numel()
+
+
+# ---------------------------------------------------------------------------- embedding
+def embed_workspace(tokens: int, vocab: int, dim: int, device="cuda",
+                    stream=None) -> torch.Tensor:
+    """A fresh workspace for embed and embed_grad of up to `tokens` tokens."""
+    return _workspace("casgd_embed_workspace_size", int(tokens), int(vocab), int(dim),
+                      device=device, stream=stream)
+
+
+def embed(table: torch.Tensor, tokens: torch.Tensor, out: torch.Tensor, ws: torch.Tensor,
+          scale: float = 1.0, padding_id: int = -1, stream=None) -> torch.Tensor:
+    """out[i] = scale * table[tokens[i]]; zeros for padding_id.  Returns out."""
+    t, i, o = _matrix(table, "table"), _tokens(tokens, "tokens"), _matrix(out, "out")
+    if o.rows != i.count or o.cols != t.cols:
+        raise ValueError(f"out must be {i.count} x {t.cols}, is {o.rows} x {o.cols}")
+    _check(load().casgd_embed(C.byref(t), C.byref(i), scale, padding_id, C.byref(o), *_ws(ws),
+                              _stream(stream)), "casgd_embed")
+    return out
+
+
+def embed_grad(dout: torch.Tensor, tokens: torch.Tensor, grad: torch.Tensor, ws: torch.Tensor,
+               scale: float = 1.0, padding_id: int = -1, accumulate: bool = False,
+               stream=None) -> torch.Tensor:
+    """grad[v] = scale * sum of dout[i] over tokens[i] == v (every row of grad is written),
+    or += with accumulate (only rows named by a token are).  With scale = -eta and the
+    FP32 table as grad, accumulate is the SGD update of the table.  Returns grad."""
+    d, i, g = _matrix(dout, "dout"), _tokens(tokens, "tokens"), _matrix(grad, "grad")
+    if d.rows != i.count or d.cols != g.cols:
+        raise ValueError(f"dout must be {i.count} x {g.cols}, is {d.rows} x {d.cols}")
+    _check(load().casgd_embed_grad(C.byref(d), C.byref(i), scale, padding_id,
+                                   1 if accumulate else 0, C.byref(g), *_ws(ws),
+                                   _stream(stream)), "casgd_embed_grad")
+    return grad
+
+
+# ------------------------------------------------------------------------------ experts
+def _group(x, w, y, offsets) -> Group:
+    mx, my = _matrix(x, "x"), _matrix(y, "y")
+    if not isinstance(w, torch.Tensor) or w.dim() != 3:
+        raise ValueError("w must be a 3-D experts x n x k tensor")
+    e, n, k = w.shape
+    if not 1 <= e <= MAX_GROUPS:
+        raise ValueError(f"w must have 1 to {MAX_GROUPS} experts, has {e}")
+    if mx.dtype == CASGD_F32 or w.dtype != x.dtype or y.dtype != x.dtype:
+        raise ValueError("x, w and y must all be bfloat16 or all float16")
+    if mx.rows != my.rows or mx.cols != k or my.cols != n:
+        raise ValueError(f"x must be rows x {k} and y rows x {n}, are {tuple(x.shape)} and "
+                         f"{tuple(y.shape)}")
+    se, ld, inner = w.stride()
+    if n == 1:
+        ld = max(ld, k)
+    if (inner != 1 and k > 1) or ld < k or (e > 1 and se < (n - 1) * ld + k):
+        raise ValueError("w must have contiguous rows, one expert after another")
+    if not w.is_cuda:
+        raise ValueError("w must be a CUDA tensor")
+    off = None
+    if offsets is not None:
+        off = _vector(offsets, "offsets", torch.int32, e + 1)
+    return Group(mx.rows, e, k, n, mx.dtype, off, mx.data, mx.ld, w.data_ptr(), ld, se, my.data,
+                 my.ld)
+
+
+def group_workspace(x: torch.Tensor, w: torch.Tensor, y: torch.Tensor,
+                    stream=None) -> torch.Tensor:
+    """A fresh workspace for the three products of rows x (rows x k), experts w (experts x
+    n x k) and outputs y (rows x n); tensors of their shapes, strides and alignment."""
+    return _workspace("casgd_group_workspace_size", C.byref(_group(x, w, y, None)),
+                      device=x.device, stream=stream)
+
+
+def _group_call(name, x, w, y, offsets, ws, stream):
+    g = _group(x, w, y, offsets)
+    _check(getattr(load(), name)(C.byref(g), *_ws(ws), _stream(stream)), name)
+
+
+def group_product(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, y: torch.Tensor,
+                  ws: torch.Tensor, stream=None) -> torch.Tensor:
+    """y[i] = x[i] w[e]^T for the rows i of expert e, offsets[e] <= i < offsets[e+1]
+    (offsets: int32, experts + 1).  Returns y."""
+    _group_call("casgd_group_product", x, w, y, offsets, ws, stream)
+    return y
+
+
+def group_product_dx(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
+                     dx: torch.Tensor, ws: torch.Tensor, stream=None) -> torch.Tensor:
+    """dx[i] = dy[i] w[e]: group_product's gradient by its rows.  Returns dx."""
+    _group_call("casgd_group_product_dx", dx, w, dy, offsets, ws, stream)
+    return dx
+
+
+def group_product_dw(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor,
+                     dw: torch.Tensor, ws: torch.Tensor, stream=None) -> torch.Tensor:
+    """dw[e] = dy_e^T x_e: group_product's gradient by its experts.  Returns dw."""
+    _group_call("casgd_group_product_dw", x, dw, dy, offsets, ws, stream)
+    return dw
+
+
+# ------------------------------------------------------------------------------- losses
+@dataclass
+class PreferenceOut:
+    loss: torch.Tensor     # [1]
+    margin: torch.Tensor   # [pairs]
+    logp: torch.Tensor     # [2 * pairs]
+
+    @classmethod
+    def alloc(cls, pairs: int, device="cuda") -> "PreferenceOut":
+        return cls(*(torch.empty(n, dtype=torch.float32, device=device)
+                     for n in (1, pairs, 2 * pairs)))
+
+
+@dataclass
+class PolicyOut:
+    stats: torch.Tensor    # [3]: loss, KL term, weight of the clipped rows
+    logp: torch.Tensor     # [rows]
+
+    @classmethod
+    def alloc(cls, rows: int, device="cuda") -> "PolicyOut":
+        return cls(*(torch.empty(n, dtype=torch.float32, device=device) for n in (3, rows)))
+
+
+def _rows(logits, targets, grad) -> tuple:
+    x, t = _matrix(logits, "logits"), _tokens(targets, "targets")
+    if t.count != x.rows:
+        raise ValueError(f"targets must have {x.rows} elements, has {t.count}")
+    if grad is None:
+        return x, t, None
+    g = _matrix(grad, "grad")
+    if (g.rows, g.cols, g.dtype) != (x.rows, x.cols, x.dtype):
+        raise ValueError("grad must have the logits' shape and type")
+    return x, t, C.byref(g)
+
+
+def preference_workspace(rows: int, pairs: int, device="cuda", stream=None) -> torch.Tensor:
+    return _workspace("casgd_preference_workspace_size", int(rows), int(pairs), device=device,
+                      stream=stream)
+
+
+def preference_loss(logits: torch.Tensor, targets: torch.Tensor, seq_offsets: torch.Tensor,
+                    ref_logp: torch.Tensor, grad: torch.Tensor | None, out: PreferenceOut,
+                    ws: torch.Tensor, beta: float = 0.1, kind: int = CASGD_LOGISTIC,
+                    smoothing: float = 0.0, mean: bool = False, grad_scale: float = 1.0,
+                    stream=None) -> PreferenceOut:
+    """Preference loss of pairs of sequences (2p chosen, 2p+1 rejected; seq_offsets: int32,
+    2 * pairs + 1) and its gradient by the logits (grad; None: the loss alone).  A negative
+    target masks its row.  grad may be logits itself.  Returns out."""
+    x, t, g = _rows(logits, targets, grad)
+    pairs = out.margin.numel()
+    _check(load().casgd_preference_loss(
+        C.byref(x), C.byref(t), _vector(seq_offsets, "seq_offsets", torch.int32, 2 * pairs + 1),
+        pairs, _vector(ref_logp, "ref_logp", torch.float32, 2 * pairs),
+        C.byref(PreferenceParams(beta, kind, smoothing, 1 if mean else 0, grad_scale)),
+        _vector(out.loss, "out.loss", torch.float32, 1),
+        _vector(out.margin, "out.margin", torch.float32, pairs),
+        _vector(out.logp, "out.logp", torch.float32, 2 * pairs), g, *_ws(ws), _stream(stream)),
+        "casgd_preference_loss")
+    return out
+
+
+def policy_workspace(rows: int, device="cuda", stream=None) -> torch.Tensor:
+    return _workspace("casgd_policy_workspace_size", int(rows), device=device, stream=stream)
+
+
+def policy_loss(logits: torch.Tensor, targets: torch.Tensor, weights: torch.Tensor,
+                old_logp: torch.Tensor, adv: torch.Tensor, grad: torch.Tensor | None,
+                out: PolicyOut, ws: torch.Tensor, ref_logp: torch.Tensor | None = None,
+                kl: float = 0.0, clip_low: float = 0.2, clip_high: float = 0.2,
+                temperature: float = 1.0, grad_scale: float = 1.0, stream=None) -> PolicyOut:
+    """Clipped policy loss of sampled tokens with a KL term (ref_logp), and its gradient by
+    the logits (grad; None: the loss and log probabilities alone).  weights: each row's
+    factor in the sums.  grad may be logits itself.  Returns out."""
+    x, t, g = _rows(logits, targets, grad)
+    n, f32 = x.rows, torch.float32
+    _check(load().casgd_policy_loss(
+        C.byref(x), C.byref(t), _vector(weights, "weights", f32, n),
+        _vector(old_logp, "old_logp", f32, n),
+        None if ref_logp is None else _vector(ref_logp, "ref_logp", f32, n),
+        _vector(adv, "adv", f32, n),
+        C.byref(PolicyParams(kl, clip_low, clip_high, temperature, grad_scale)),
+        _vector(out.stats, "out.stats", f32, 3), _vector(out.logp, "out.logp", f32, n), g,
+        *_ws(ws), _stream(stream)), "casgd_policy_loss")
+    return out

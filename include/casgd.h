@@ -443,6 +443,155 @@ int casgd_sgd_fp32(const float* X, int64_t m, int64_t n, int64_t ld, const float
 int casgd_chain_trace(const casgd_data_t* data, const casgd_params_t* params, void* ws,
                       size_t ws_bytes, void* stream, uint64_t* out);
 
+/* ------------------------------------------------------------------------------------
+ * Token models: the operators that one SGD step of a model over tokens needs beside the
+ * generalized linear models above -- features looked up by token, linear models chosen
+ * per row (experts), and losses on log probabilities -- each with its gradient.  A
+ * preference loss is the GLM loss l(z, +1) of a pair's margin z.
+ *
+ * Every call takes a workspace: 256-byte aligned, of the size its *_workspace_size call
+ * gives, initialised once with casgd_workspace_init, owned by the caller and used by one
+ * stream at a time.  Calls are asynchronous; CASGD_ERR_BAD_INDEX found on the device is
+ * sticky in the workspace (casgd_get_status).  Nothing outside the given arrays is read
+ * or written whatever the token numbers and offsets hold.  Sums are FP32 or wider in a
+ * fixed order (the same call on the same inputs gives the same bits), rounded once to
+ * the output's type.  Inputs and outputs must not overlap except where stated.
+ * ---------------------------------------------------------------------------------- */
+
+/* Element types of the matrices below. */
+enum { CASGD_F32 = 0, CASGD_BF16 = 1, CASGD_F16 = 2 };
+
+/* Row-major device matrix; data aligned to its element; ld >= cols elements from row to
+ * row.  Rows that start on 16-byte boundaries are read and written faster. */
+typedef struct {
+  void* data;
+  int64_t rows, cols, ld;
+  int32_t dtype;       /* CASGD_F32 / CASGD_BF16 / CASGD_F16 */
+} casgd_matrix_t;
+
+/* Token numbers: device int32 (wide = 0) or int64 (wide = 1). */
+typedef struct {
+  const void* data;
+  int64_t count;
+  int32_t wide;
+} casgd_tokens_t;
+
+/* Bytes of workspace casgd_embed and casgd_embed_grad need for `rows` tokens and a
+ * vocab x dim table.  rows, vocab, dim < 2^31.  Host only. */
+int casgd_embed_workspace_size(int64_t rows, int64_t vocab, int64_t dim, size_t* bytes);
+
+/* Embedding lookup: out[i] = scale * table[tokens[i]], one FP32 product per element
+ * rounded to out's type.  A token equal to padding_id gives zeros (-1: the usual value
+ * where there is none); any other token outside [0, table->rows) gives zeros and
+ * CASGD_ERR_BAD_INDEX.  out: tokens->count x table->cols. */
+int casgd_embed(const casgd_matrix_t* table, const casgd_tokens_t* tokens, float scale,
+                int64_t padding_id, const casgd_matrix_t* out, void* ws, size_t ws_bytes,
+                void* stream);
+
+/* Gradient of the lookup: grad[v] = scale * sum of dout[i] over the i with tokens[i] = v,
+ * and zeros for rows v that no token names; with `accumulate`, grad[v] += that sum and
+ * other rows are not touched -- on an FP32 table with scale times -eta this is the SGD
+ * update of the table itself.  Padding and out-of-range tokens add nothing (the latter
+ * set CASGD_ERR_BAD_INDEX).  The rows of equal tokens are added in a fixed order in
+ * FP32.  dout: tokens->count x dim; grad: vocab x dim. */
+int casgd_embed_grad(const casgd_matrix_t* dout, const casgd_tokens_t* tokens, float scale,
+                     int64_t padding_id, int32_t accumulate, const casgd_matrix_t* grad,
+                     void* ws, size_t ws_bytes, void* stream);
+
+/* Matrix products grouped by expert.  Rows are sorted by expert: expert e has the rows
+ * offsets[e] .. offsets[e+1]-1 (device int32[groups+1], offsets[0] = 0, ascending, at
+ * most `rows`; anything else is held inside [0, rows] and sets CASGD_ERR_BAD_INDEX).  An
+ * expert may have no rows.  16-bit inputs and outputs of one type, FP32 accumulation. */
+typedef struct {
+  int64_t rows, groups, k, n;
+  int32_t dtype;           /* CASGD_BF16 or CASGD_F16 */
+  const int32_t* offsets;
+  void* x;                 /* rows x k, ldx elements from row to row */
+  int64_t ldx;
+  void* w;                 /* groups x n x k, ldw from row to row, stride_w from expert
+                              to expert */
+  int64_t ldw, stride_w;
+  void* y;                 /* rows x n */
+  int64_t ldy;
+} casgd_group_t;
+#define CASGD_MAX_GROUPS 1024
+
+/* Bytes of workspace the three calls below need for these matrices (only the sizes,
+ * strides, type and alignment of g are used).  Host only. */
+int casgd_group_workspace_size(const casgd_group_t* g, size_t* bytes);
+
+/* y = x w_e^T per row (rows after the last offset: zeros). */
+int casgd_group_product(const casgd_group_t* g, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of the rows: x receives y w_e, y holds the gradient of the outputs (rows after
+ * the last offset: zeros). */
+int casgd_group_product_dx(const casgd_group_t* g, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of the weights: w_e receives y_e^T x_e (zeros for an expert without rows), y
+ * holds the gradient of the outputs. */
+int casgd_group_product_dw(const casgd_group_t* g, void* ws, size_t ws_bytes, void* stream);
+
+/* Parameters of the preference loss. */
+typedef struct {
+  float beta;          /* factor of the margin                                      */
+  int32_t kind;        /* CASGD_LOGISTIC or CASGD_LSQ: the loss l(z, +1)            */
+  float smoothing;     /* share of l(z, -1) in the loss, in [0, 1]                  */
+  int32_t mean;        /* a sequence's log probability is the mean over its tokens,
+                          not their sum                                             */
+  float grad_scale;    /* factor of the gradient (loss scaling)                     */
+} casgd_preference_t;
+
+/* Bytes of workspace casgd_preference_loss needs.  Host only. */
+int casgd_preference_workspace_size(int64_t rows, int64_t pairs, size_t* bytes);
+
+/* Preference loss of `pairs` pairs of sequences, and its gradient by the logits.
+ * Sequence q has the rows seq_offsets[q] .. seq_offsets[q+1]-1 of logits (device
+ * int32[2*pairs + 1], ascending, within [0, rows]; else CASGD_ERR_BAD_INDEX); sequence
+ * 2p is the chosen one of pair p and 2p+1 the rejected one.  Row t's target is
+ * targets[t]; a negative target masks the row, one past the vocabulary masks it and sets
+ * CASGD_ERR_BAD_INDEX.  A masked row is not read.
+ *   lp_t  = x_t[target] - log sum exp x_t          (x_t: row t of the logits)
+ *   logp_q = sum (or mean) of lp_t over the unmasked rows of q; 0 when there is none
+ *   z_p   = beta * ((logp_2p - ref_2p) - (logp_2p+1 - ref_2p+1))
+ *   loss  = mean over p of (1-smoothing) * l(z_p, +1) + smoothing * l(z_p, -1)
+ * ref_logp: device FP32[2*pairs].  Outputs: loss FP32[1], margin FP32[pairs], logp
+ * FP32[2*pairs], and (grad not NULL) grad_scale * d loss / d logits, of the logits' type
+ * and shape, zeros in masked rows and in rows of no sequence.  grad->data may be
+ * logits->data with the same ld. */
+int casgd_preference_loss(const casgd_matrix_t* logits, const casgd_tokens_t* targets,
+                          const int32_t* seq_offsets, int64_t pairs, const float* ref_logp,
+                          const casgd_preference_t* params, float* loss, float* margin,
+                          float* logp, const casgd_matrix_t* grad, void* ws, size_t ws_bytes,
+                          void* stream);
+
+/* Parameters of the policy loss. */
+typedef struct {
+  float kl;            /* factor of the KL term                                     */
+  float clip_low;      /* the ratio is held in [1 - clip_low, 1 + clip_high]        */
+  float clip_high;
+  float temperature;   /* > 0: the logits are divided by it                         */
+  float grad_scale;    /* factor of the gradient (loss scaling)                     */
+} casgd_policy_t;
+
+/* Bytes of workspace casgd_policy_loss needs.  Host only. */
+int casgd_policy_workspace_size(int64_t rows, size_t* bytes);
+
+/* Clipped policy loss over sampled tokens, and its gradient by the logits.  Targets as in
+ * casgd_preference_loss.  weights: device FP32[rows], each row's factor in the sums (its
+ * mask and its normalisation); a row of weight 0 adds nothing, whatever its other inputs
+ * hold, and has a zero gradient.
+ *   lp_t = x_t[target]/temperature - log sum exp (x_t/temperature);  r = exp(lp_t - old_t)
+ *   k_t  = exp(ref_t - lp_t) - (ref_t - lp_t) - 1        (0 when ref_logp is NULL)
+ *   L_t  = -min(r adv_t, clip(r) adv_t) + kl * k_t
+ * old_logp, ref_logp, adv: device FP32[rows].  Outputs: stats FP32[3] = the sums of
+ * weight * L, weight * k and weight * [the clip is active]; logp FP32[rows] = lp (0 in
+ * masked rows); and (grad not NULL) grad_scale * d(sum of weight * L) / d logits, as in
+ * casgd_preference_loss. */
+int casgd_policy_loss(const casgd_matrix_t* logits, const casgd_tokens_t* targets,
+                      const float* weights, const float* old_logp, const float* ref_logp,
+                      const float* adv, const casgd_policy_t* params, float* stats, float* logp,
+                      const casgd_matrix_t* grad, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,203 @@
+"""Refusals of the token-model operators: what the binding rejects before the library is
+called, and what the C entry points reject before any CUDA call.  No GPU."""
+import ctypes as C
+
+import pytest
+import torch
+
+import communication_avoiding_step_gb300 as casgd
+from communication_avoiding_step_gb300 import _native as nat
+
+FAKE = 1 << 20          # an address that is never dereferenced: every case fails first
+P = C.c_void_p
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return casgd.load()
+
+
+def mat(rows=4, cols=8, ld=None, dtype=nat.CASGD_BF16, data=FAKE):
+    return nat.Matrix(data, rows, cols, cols if ld is None else ld, dtype)
+
+
+def tok(count=4, wide=1, data=FAKE):
+    return nat.Tokens(data, count, wide)
+
+
+BAD_MATRICES = [mat(cols=0), mat(rows=-1), mat(ld=7), mat(dtype=3), mat(dtype=-1),
+                mat(data=None), mat(data=FAKE + 1), mat(rows=1 << 31), mat(ld=1 << 31)]
+
+
+def test_sizes(lib):
+    n = C.c_size_t(0)
+    assert lib.casgd_embed_workspace_size(100, 1000, 64, C.byref(n)) == 0
+    assert n.value % 256 == 0 and n.value >= 100 * 16
+    assert lib.casgd_embed_workspace_size(0, 1, 1, C.byref(n)) == 0 and n.value >= 256
+    assert lib.casgd_preference_workspace_size(10, 1, C.byref(n)) == 0 and n.value % 256 == 0
+    assert lib.casgd_policy_workspace_size(0, C.byref(n)) == 0 and n.value >= 256
+    for call, args in (("embed", (-1, 5, 5)), ("embed", (5, 0, 5)), ("embed", (5, 5, 0)),
+                       ("embed", (5, 1 << 31, 5)), ("preference", (5, 0)),
+                       ("preference", (-1, 1)), ("policy", (-1,)), ("policy", (1 << 31,))):
+        fn = getattr(lib, f"casgd_{call}_workspace_size")
+        assert fn(*args, C.byref(n)) == nat.CASGD_ERR_ARG
+        assert fn(*([3] * len(args)), None) == nat.CASGD_ERR_ARG
+
+
+def test_embed_refusals(lib):
+    def embed(t=None, i=None, o=None, ws=FAKE, nbytes=1 << 30):
+        t, i, o = t or mat(), i or tok(), o or mat()
+        return lib.casgd_embed(C.byref(t), C.byref(i), 1.0, -1, C.byref(o), P(ws), nbytes, None)
+
+    def grad(d=None, i=None, g=None, acc=0, ws=FAKE, nbytes=1 << 30):
+        d, i, g = d or mat(), i or tok(), g or mat(rows=9)
+        return lib.casgd_embed_grad(C.byref(d), C.byref(i), 1.0, -1, acc, C.byref(g), P(ws),
+                                    nbytes, None)
+
+    for m in BAD_MATRICES:
+        assert embed(t=m) == embed(o=m) == grad(d=m) == grad(g=m) == nat.CASGD_ERR_ARG
+    for i in (tok(count=-1), tok(wide=2), tok(data=None), tok(data=FAKE + 4), tok(count=3)):
+        assert embed(i=i) == grad(i=i) == nat.CASGD_ERR_ARG
+    assert embed(t=mat(rows=0)) == grad(g=mat(rows=0)) == nat.CASGD_ERR_ARG
+    assert embed(o=mat(cols=7)) == grad(g=mat(cols=9)) == nat.CASGD_ERR_ARG
+    assert grad(acc=2) == nat.CASGD_ERR_ARG
+    for call in (embed, grad):
+        assert call(ws=None) == call(ws=FAKE + 8) == call(nbytes=8) == nat.CASGD_ERR_WORKSPACE
+
+
+def group(**kw):
+    d = dict(rows=16, groups=2, k=8, n=24, dtype=nat.CASGD_BF16, offsets=FAKE, x=FAKE, ldx=8,
+             w=FAKE, ldw=8, stride_w=192, y=FAKE, ldy=24)
+    d.update(kw)
+    return nat.Group(**d)
+
+
+def test_group_refusals(lib):
+    n = C.c_size_t(0)
+    assert lib.casgd_group_workspace_size(C.byref(group()), C.byref(n)) == 0 and n.value > 0
+    bad = [dict(rows=-1), dict(rows=1 << 31), dict(groups=0), dict(groups=1025), dict(k=0),
+           dict(n=0), dict(dtype=nat.CASGD_F32), dict(dtype=5), dict(ldx=7), dict(ldw=7),
+           dict(ldy=23), dict(stride_w=191)]
+    for b in bad:
+        g = group(**b)
+        assert lib.casgd_group_workspace_size(C.byref(g), C.byref(n)) == nat.CASGD_ERR_ARG
+    bad += [dict(offsets=None), dict(offsets=FAKE + 2), dict(x=None), dict(w=None), dict(y=None),
+            dict(x=FAKE + 1), dict(w=FAKE + 1), dict(y=FAKE + 1)]
+    for name in ("casgd_group_product", "casgd_group_product_dx", "casgd_group_product_dw"):
+        call = getattr(lib, name)
+        for b in bad:
+            assert call(C.byref(group(**b)), P(FAKE), 1 << 40, None) == nat.CASGD_ERR_ARG
+        for ws, nb in ((None, 1 << 40), (FAKE + 8, 1 << 40), (FAKE, 16)):
+            assert call(C.byref(group()), P(ws), nb, None) == nat.CASGD_ERR_WORKSPACE
+        assert call(None, P(FAKE), 1 << 40, None) == nat.CASGD_ERR_ARG
+
+
+def test_loss_refusals(lib):
+    def pref(x=None, t=None, g=None, pairs=2, ws=FAKE, nbytes=1 << 30, ptrs=(FAKE,) * 5, **kw):
+        d = dict(beta=0.1, kind=0, smoothing=0.0, mean=0, grad_scale=1.0)
+        d.update(kw)
+        x, t = x or mat(), t or tok()
+        p = [P(v) if v else None for v in ptrs]
+        return lib.casgd_preference_loss(
+            C.byref(x), C.byref(t), p[0], pairs, p[1], C.byref(nat.PreferenceParams(**d)), p[2],
+            p[3], p[4], C.byref(g) if g else None, P(ws), nbytes, None)
+
+    def policy(x=None, t=None, g=None, ws=FAKE, nbytes=1 << 30, ptrs=(FAKE,) * 6, **kw):
+        d = dict(kl=0.0, clip_low=0.2, clip_high=0.2, temperature=1.0, grad_scale=1.0)
+        d.update(kw)
+        x, t = x or mat(), t or tok()
+        p = [P(v) if v else None for v in ptrs]
+        return lib.casgd_policy_loss(
+            C.byref(x), C.byref(t), p[0], p[1], p[2], p[3], C.byref(nat.PolicyParams(**d)), p[4],
+            p[5], C.byref(g) if g else None, P(ws), nbytes, None)
+
+    nan = float("nan")
+    for call in (pref, policy):
+        for m in BAD_MATRICES:
+            assert call(x=m) == call(g=m) == nat.CASGD_ERR_ARG
+        assert call(t=tok(count=5)) == call(t=tok(wide=3)) == nat.CASGD_ERR_ARG
+        for g in (mat(rows=5), mat(cols=7), mat(dtype=nat.CASGD_F16), mat(ld=16)):
+            assert call(g=g) == nat.CASGD_ERR_ARG       # the last: in place with another pitch
+        assert call(grad_scale=nan) == nat.CASGD_ERR_ARG
+        assert call(ws=None) == call(ws=FAKE + 4) == call(nbytes=300) == nat.CASGD_ERR_WORKSPACE
+    for e in range(5):
+        for v in (None, FAKE + 2):
+            assert pref(ptrs=[v if j == e else FAKE for j in range(5)]) == nat.CASGD_ERR_ARG
+    for e in (0, 1, 3, 4, 5):                            # ref_logp may be null
+        assert policy(ptrs=[None if j == e else FAKE for j in range(6)]) == nat.CASGD_ERR_ARG
+    assert policy(ptrs=[FAKE, FAKE, FAKE + 2, FAKE, FAKE, FAKE]) == nat.CASGD_ERR_ARG
+    for kw in (dict(pairs=0), dict(kind=nat.CASGD_POISSON), dict(kind=-1), dict(beta=nan),
+               dict(smoothing=-0.1), dict(smoothing=1.1), dict(smoothing=nan), dict(mean=2)):
+        assert pref(**kw) == nat.CASGD_ERR_ARG
+    for kw in (dict(kl=nan), dict(clip_low=-0.1), dict(clip_high=nan), dict(temperature=0.0),
+               dict(temperature=-1.0), dict(temperature=nan)):
+        assert policy(**kw) == nat.CASGD_ERR_ARG
+
+
+def test_binding_refuses_before_the_library(monkeypatch):
+    """Shapes, types, layouts and devices that would let the library read or write past a
+    tensor are refused by the binding (checked with CPU tensors and no library)."""
+    from communication_avoiding_step_gb300 import token_ops
+
+    def no_library():
+        raise AssertionError("the library was called")
+
+    monkeypatch.setattr(token_ops, "load", no_library)
+    f, ids = torch.zeros(4, 8), torch.zeros(4, dtype=torch.int64)
+    ws = torch.zeros(1024, dtype=torch.uint8)
+    for table in (f.double(), f[0], f.t(), f[:, ::2], f.expand(3, 4, 8), f[:1].expand(4, 8), "x"):
+        with pytest.raises(ValueError, match="table"):
+            casgd.embed(table, ids, f, ws)
+    with pytest.raises(ValueError, match="CUDA"):
+        casgd.embed(f, ids, f, ws)
+    with pytest.raises(ValueError, match="CUDA"):
+        casgd.embed_grad(f, ids, f, ws)
+    x, w = f.bfloat16(), torch.zeros(2, 8, 8, dtype=torch.bfloat16)
+    off = torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        casgd.group_product(x, w, off, x, ws)
+    out = casgd.PreferenceOut.alloc(1, device="cpu")
+    with pytest.raises(ValueError, match="CUDA"):
+        casgd.preference_loss(f, ids, off, f[0], f, out, ws)
+    pol = casgd.PolicyOut.alloc(4, device="cpu")
+    with pytest.raises(ValueError, match="CUDA"):
+        casgd.policy_loss(f, ids, f[0], f[0], f[0], f, pol, ws)
+
+
+@pytest.mark.gpu
+def test_binding_refuses_wrong_shapes():
+    f = torch.zeros(4, 8, device="cuda")
+    b, ids = f.bfloat16(), torch.zeros(4, dtype=torch.int64, device="cuda")
+    ws = casgd.embed_workspace(4, 4, 8)
+    w = torch.zeros(2, 8, 8, dtype=torch.bfloat16, device="cuda")
+    off = torch.zeros(3, dtype=torch.int32, device="cuda")
+    v = torch.zeros(8, device="cuda")
+    with pytest.raises(ValueError):
+        casgd.embed(f, ids[:3], f, ws)                  # out has a row too many
+    with pytest.raises(ValueError):
+        casgd.embed(f, ids.float(), f, ws)
+    with pytest.raises(ValueError):
+        casgd.embed_grad(f, ids, f[:, :7], ws)
+    with pytest.raises(ValueError):
+        casgd.embed(f, ids, f.clone(), ws.float())
+    with pytest.raises(casgd.CasgdError) as e:
+        casgd.embed_grad(f, ids, f.clone(), ws[:256])
+    assert e.value.code == 2
+    gws = casgd.group_workspace(b, w, b)
+    for args in ((f, w, off, b), (b, w[0], off, b), (b, w, off[:2], b), (b, w, off.long(), b),
+                 (b, w.half(), off, b), (b[:3], w, off, b), (b, w.transpose(1, 2), off, b)):
+        with pytest.raises(ValueError):
+            casgd.group_product(*args, gws)
+    out = casgd.PreferenceOut.alloc(1)
+    pws = casgd.preference_workspace(4, 1)
+    for args in ((f, ids[:3], off, v, f), (f, ids, off[:2], v, f), (f, ids, off, v[:1], f),
+                 (f, ids, off, v, b), (f, ids, off, v, f[:3]), (f, ids, off.long(), v, f)):
+        with pytest.raises(ValueError):
+            casgd.preference_loss(*args, out, pws)
+    pol, qws = casgd.PolicyOut.alloc(4), casgd.policy_workspace(4)
+    for args in ((f, ids, v[:3], v, v, f), (f, ids, v, v.double(), v, f),
+                 (f, ids, v, v, v[:2], f)):
+        with pytest.raises(ValueError):
+            casgd.policy_loss(*args, pol, qws)
+    with pytest.raises(ValueError):
+        casgd.policy_loss(f, ids, v, v, v, f, casgd.PolicyOut.alloc(3), qws)
