@@ -72,7 +72,7 @@ int group_call(GroupDir dir, const casgd_group_t* g, void* ws, size_t ws_bytes, 
   if (rc != CASGD_OK) return rc;
   Ctx c{};
   if ((rc = make_ctx(stream, c)) != CASGD_OK) return rc;
-  return done(launch_group(dir, group_args(g), static_cast<Ctrl*>(ws), c));
+  return done(launch_group(dir, group_args(g), ws, c));
 }
 
 // Logits, targets and an optional gradient of the logits' shape and type.
@@ -128,7 +128,7 @@ int casgd_embed_grad(const casgd_matrix_t* dout, const casgd_tokens_t* tokens, f
 
 int casgd_group_workspace_size(const casgd_group_t* g, size_t* bytes) {
   if (!bytes || !check_group(g)) return CASGD_ERR_ARG;
-  *bytes = 512;
+  *bytes = group_workspace_bytes(group_args(g));
   return CASGD_OK;
 }
 

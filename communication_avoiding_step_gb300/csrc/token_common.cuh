@@ -83,7 +83,8 @@ struct GroupArgs {
   void* y;   // rows x n
   int64_t ldy;
 };
-cudaError_t launch_group(GroupDir dir, const GroupArgs& g, Ctrl* ctrl, Ctx& c);
+size_t group_workspace_bytes(const GroupArgs& g);
+cudaError_t launch_group(GroupDir dir, const GroupArgs& g, void* ws, Ctx& c);
 
 // ------------------------------------------------------------------ losses (k_row_loss.cu)
 struct PrefArgs {
