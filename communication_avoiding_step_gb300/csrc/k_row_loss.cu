@@ -3,10 +3,20 @@
 //
 // Both need, of each row x, the target's log probability
 //   lp = x[target] - max - log(sum of exp(x - max))
-// and then write g * (onehot(target) - softmax(x)) for a factor g of the row.  A row's
-// exponentials are summed against the largest value the thread has seen (a running
-// maximum and sum), and the threads' pairs are joined once per row.  All of it is in
-// FP32, rounded once to the logits' type.
+// and then write g * (onehot(target) - softmax(x)) for a factor g of the row.  One
+// exponential per element and pass, so the bytes of the logits and of the gradient bound
+// them.  All of it is in FP32, rounded once to the logits' type.
+//
+//   Policy loss: g depends on the row alone, so a row is read once.  It is held on chip
+//   between its sum and its gradient (policy_kernel).
+//   Preference loss: g depends on every row of both sequences of a pair, which do not fit
+//   on chip, so the rows are read twice (pref_stats_kernel, pref_grad_kernel) with the
+//   pairs' sums between (pref_pair_kernel).
+//
+// Rows are handled in 16-byte granules of memory, counted from the granule that holds the
+// row's first element, so that rows at any alignment take the same path; the granules that
+// hold elements of other rows too (at most the first and the last) go element by element.
+#include "ptx_async.cuh"
 #include "token_common.cuh"
 
 namespace casgd {
@@ -14,58 +24,165 @@ namespace {
 
 constexpr size_t kAlign = 256;
 inline size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
-constexpr int kRowThreads = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 
-// A maximum m and the sum s of exp2(t - m) over the values t seen (m = -inf, s = 0: none).
-struct MaxSum {
-  float m, s;
-};
-__device__ __forceinline__ float exp2_diff(float t, float m) {
-  return t == m ? 1.0f : exp2f(t - m);  // equal infinities count as one
-}
-__device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b) {
-  const float m = fmaxf(a.m, b.m);
-  if (m == -INFINITY) return {m, a.s + b.s};
-  return {m, a.s * exp2_diff(a.m, m) + b.s * exp2_diff(b.m, m)};
-}
-
-template <class T>
-__device__ MaxSum row_max_sum(const T* x, int64_t n, float scale2) {
-  MaxSum r{-INFINITY, 0.0f};
-  for (int64_t i = threadIdx.x; i < n; i += kRowThreads) {
-    const float t = Elem<T>::get(x[i]) * scale2;
-    if (t > r.m) {
-      r.s = r.s * exp2f(r.m - t) + 1.0f;
-      r.m = t;
-    } else {
-      r.s += t == -INFINITY ? 0.0f : exp2_diff(t, r.m);  // NaN stays NaN
-    }
-  }
-  __shared__ MaxSum part[kRowThreads / 32];
-#pragma unroll
-  for (int o = 16; o > 0; o /= 2)
-    r = join(r, {__shfl_xor_sync(0xffffffffu, r.m, o), __shfl_xor_sync(0xffffffffu, r.s, o)});
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = r;
-  __syncthreads();
-  r = part[0];
-  for (int w = 1; w < kRowThreads / 32; ++w) r = join(r, part[w]);
+// 2^t; results below the normal range are zero.
+__device__ __forceinline__ float fast_exp2(float t) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
   return r;
 }
 
-// g * (onehot - softmax) of a row; `zero`: zeros whatever the row holds.
+// The largest value m seen and the sum s of exp2((x - m) * scale) over the values seen
+// (m = -inf, s = 0: none).
+struct MaxSum {
+  float m, s;
+};
+__device__ __forceinline__ float rescale(float m, float top, float scale) {
+  return m == top ? 1.0f : fast_exp2((m - top) * scale);
+}
+__device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b, float scale) {
+  const float m = fmaxf(a.m, b.m);
+  return {m, a.s * rescale(a.m, m, scale) + b.s * rescale(b.m, m, scale)};
+}
+template <int kLanes>
+__device__ __forceinline__ MaxSum join_lanes(MaxSum r, float scale) {
+  float m = r.m;
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float s = r.s * rescale(r.m, m, scale);
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return {m, s};
+}
+
+// A row as granules of kV elements: element 0 is element `shift` of granule 0.
 template <class T>
-__device__ void row_grad(const T* x, T* out, int64_t n, float scale2, MaxSum r, int64_t target,
-                         float g, bool zero) {
-  const float inv = 1.0f / r.s;
-  for (int64_t i = threadIdx.x; i < n; i += kRowThreads) {
-    float v = 0.0f;
-    if (!zero) {
-      const float p = exp2f(Elem<T>::get(x[i]) * scale2 - r.m) * inv;
-      v = g * ((i == target ? 1.0f : 0.0f) - p);
+struct Row {
+  static constexpr int kV = 16 / sizeof(T);
+  const T* x;   // element 0
+  int64_t n;
+  int shift;
+  int64_t granules;
+  __device__ __forceinline__ Row(const T* p, int64_t cols)
+      : x(p), n(cols), shift((int)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T))),
+        granules((cols + shift + kV - 1) / kV) {}
+  __device__ __forceinline__ int64_t first(int64_t g) const { return g * kV - shift; }
+  __device__ __forceinline__ bool whole(int64_t g) const {
+    return first(g) >= 0 && first(g) + kV <= n;
+  }
+  // granule g; -inf in the places of other rows' elements
+  __device__ __forceinline__ void load(int64_t g, float (&v)[kV]) const {
+    const int64_t i = first(g);
+    if (whole(g)) {
+      const Pack<T, kV> p = *reinterpret_cast<const Pack<T, kV>*>(x + i);
+#pragma unroll
+      for (int e = 0; e < kV; ++e) v[e] = Elem<T>::get(p.v[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kV; ++e)
+        v[e] = i + e >= 0 && i + e < n ? Elem<T>::get(x[i + e]) : -INFINITY;
     }
-    out[i] = Elem<T>::put(v);
+  }
+};
+
+// Granule g of a gradient row (element 0 at `out`), laid over the granules of `r`.
+template <class T>
+__device__ __forceinline__ void put_granule(const Row<T>& r, T* out, bool aligned, int64_t g,
+                                            const float (&v)[Row<T>::kV]) {
+  constexpr int kV = Row<T>::kV;
+  Pack<T, kV> p;
+#pragma unroll
+  for (int e = 0; e < kV; ++e) p.v[e] = Elem<T>::put(v[e]);
+  const int64_t i = r.first(g);
+  if (aligned && r.whole(g)) {
+    *reinterpret_cast<Pack<T, kV>*>(out + i) = p;
+  } else {
+#pragma unroll
+    for (int e = 0; e < kV; ++e)
+      if (i + e >= 0 && i + e < r.n) out[i + e] = p.v[e];
+  }
+}
+template <class T>
+__device__ __forceinline__ bool same_phase(const T* a, const T* b) {
+  return ((reinterpret_cast<uintptr_t>(a) ^ reinterpret_cast<uintptr_t>(b)) & 15) == 0;
+}
+
+// Maximum and sum of a row by kT threads (a warp, or a block of kT); every thread gets them.
+template <class T, int kT>
+__device__ MaxSum row_max_sum(const Row<T>& r, int tid, float scale) {
+  constexpr int kV = Row<T>::kV, kU = 4;
+  MaxSum acc{-INFINITY, 0.0f};
+  for (int64_t g0 = tid; g0 < r.granules; g0 += kT * kU) {
+    float v[kU][kV];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      if (g0 + u * kT < r.granules) {
+        r.load(g0 + u * kT, v[u]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < kV; ++e) v[u][e] = -INFINITY;
+      }
+    }
+    float m = acc.m;
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+#pragma unroll
+      for (int e = 0; e < kV; ++e) m = fmaxf(m, v[u][e]);
+    const float base = m == -INFINITY ? 0.0f : m;
+    float s[kU] = {};
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+#pragma unroll
+      for (int e = 0; e < kV; ++e) s[u] += fast_exp2((v[u][e] - base) * scale);
+    acc.s = acc.s * rescale(acc.m, m, scale) + ((s[0] + s[1]) + (s[2] + s[3]));
+    acc.m = m;
+  }
+  acc = join_lanes<32>(acc, scale);
+  if (kT > 32) {
+    __shared__ MaxSum part[kT / 32];
+    __syncthreads();
+    if ((tid & 31) == 0) part[tid >> 5] = acc;
+    __syncthreads();
+    acc = join_lanes<kT / 32>(part[tid & (kT / 32 - 1)], scale);
+  }
+  return acc;
+}
+
+// The target's log probability.
+__device__ __forceinline__ float log_prob(float xt, MaxSum r, float inv_t) {
+  return (xt - r.m) * inv_t - logf(r.s);
+}
+// g * (1 - softmax) at the target
+__device__ __forceinline__ float target_grad(float g, float xt, MaxSum r, float scale) {
+  return g * (1.0f - fast_exp2((xt - r.m) * scale) / r.s);
+}
+
+// Writes g * (onehot - softmax), or zeros, for granules g0, g0 + step, .. of a row.
+template <class T>
+__device__ __forceinline__ void row_grad(const Row<T>& r, T* out, int64_t g0, int64_t g1,
+                                         int step, float scale, MaxSum ms, int64_t target,
+                                         float g, bool zero) {
+  constexpr int kV = Row<T>::kV, kU = 4;
+  const bool al = same_phase(r.x, out);
+  const float k = -g / ms.s;
+  for (int64_t i = g0; i < g1; i += (int64_t)step * kU) {
+    float v[kU][kV];
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+      if (!zero && i + (int64_t)u * step < g1) r.load(i + (int64_t)u * step, v[u]);
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int64_t gr = i + (int64_t)u * step;
+      if (gr >= g1) break;
+      const int64_t t = target - r.first(gr);
+#pragma unroll
+      for (int e = 0; e < kV; ++e) {
+        const float p = fast_exp2((v[u][e] - ms.m) * scale);
+        v[u][e] = zero ? 0.0f : t == e ? g * (1.0f - p / ms.s) : k * p;
+      }
+      put_granule(r, out, al, gr, v[u]);
+    }
   }
 }
 
@@ -91,33 +208,43 @@ struct PrefWs {
   double* loss;
 };
 
-template <class T>
-__global__ void __launch_bounds__(kRowThreads) pref_stats_kernel(PrefArgs a, PrefWs w) {
+constexpr int kBlock = 256;
+// Up to this many columns a warp takes a row, else a block: a block's two barriers cost
+// more than a warp's longer loop there.
+constexpr int64_t kWarpCols = 2048;
+
+// Each row's maximum, sum and log probability; kT threads per row.
+template <class T, int kT>
+__global__ void __launch_bounds__(kBlock) pref_stats_kernel(PrefArgs a, PrefWs w) {
   wait_prior_grid();
   allow_next_grid();
-  for (int64_t t = blockIdx.x; t < a.logits.rows; t += gridDim.x) {
+  const int tid = threadIdx.x % kT;
+  constexpr int kRows = kBlock / kT;
+  for (int64_t t = (int64_t)blockIdx.x * kRows + threadIdx.x / kT; t < a.logits.rows;
+       t += (int64_t)gridDim.x * kRows) {
     const int64_t target = a.targets.at(t);
     const bool bad = target >= a.logits.cols;
-    if (bad && threadIdx.x == 0) set_status(w.ctrl, ST_BAD_INDEX);
+    if (bad && tid == 0) set_status(w.ctrl, ST_BAD_INDEX);
     if (target < 0 || bad) {
-      if (threadIdx.x == 0) w.coef[t] = w.lp[t] = w.m[t] = w.s[t] = 0.0f;
+      if (tid == 0) w.coef[t] = w.lp[t] = w.m[t] = w.s[t] = 0.0f;
       continue;
     }
-    const T* x = static_cast<const T*>(a.logits.p) + t * a.logits.ld;
-    const MaxSum r = row_max_sum(x, a.logits.cols, kLog2e);
-    if (threadIdx.x == 0) {
+    const Row<T> row(static_cast<const T*>(a.logits.p) + t * a.logits.ld, a.logits.cols);
+    const MaxSum r = row_max_sum<T, kT>(row, tid, kLog2e);
+    if (tid == 0) {
       w.m[t] = r.m;
       w.s[t] = r.s;
       w.coef[t] = 0.0f;
-      w.lp[t] = Elem<T>::get(x[target]) - r.m / kLog2e - logf(r.s);
+      w.lp[t] = log_prob(Elem<T>::get(row.x[target]), r, 1.0f);
     }
   }
 }
 
 // One block per pair: the sequences' sums, the margin, the loss and the rows' factors.
-__global__ void __launch_bounds__(256) pref_pair_kernel(PrefArgs a, PrefWs w) {
-  __shared__ double ssum[2][8];
-  __shared__ int scnt[2][8];
+__global__ void __launch_bounds__(kBlock) pref_pair_kernel(PrefArgs a, PrefWs w) {
+  constexpr int kWarps = kBlock / 32;
+  __shared__ double ssum[2][kWarps];
+  __shared__ int scnt[2][kWarps];
   __shared__ float coef[2];
   __shared__ int last;
   wait_prior_grid();
@@ -138,7 +265,7 @@ __global__ void __launch_bounds__(256) pref_pair_kernel(PrefArgs a, PrefWs w) {
   for (int q = 0; q < 2; ++q) {
     double s = 0.0;
     int n = 0;
-    for (int64_t t = o[q] + threadIdx.x; t < o[q + 1]; t += 256) {
+    for (int64_t t = o[q] + threadIdx.x; t < o[q + 1]; t += kBlock) {
       const int64_t target = a.targets.at(t);
       if (target < 0 || target >= a.logits.cols) continue;
       s += w.lp[t];
@@ -161,7 +288,7 @@ __global__ void __launch_bounds__(256) pref_pair_kernel(PrefArgs a, PrefWs w) {
     for (int q = 0; q < 2; ++q) {
       lp[q] = 0.0;
       n[q] = 0;
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < kWarps; ++i) {
         lp[q] += ssum[q][i];
         n[q] += scnt[q][i];
       }
@@ -185,7 +312,7 @@ __global__ void __launch_bounds__(256) pref_pair_kernel(PrefArgs a, PrefWs w) {
   }
   __syncthreads();
   for (int q = 0; q < 2; ++q)
-    for (int64_t t = o[q] + threadIdx.x; t < o[q + 1]; t += 256) {
+    for (int64_t t = o[q] + threadIdx.x; t < o[q + 1]; t += kBlock) {
       const int64_t target = a.targets.at(t);
       if (target >= 0 && target < a.logits.cols) w.coef[t] = coef[q];
     }
@@ -202,17 +329,28 @@ __global__ void __launch_bounds__(256) pref_pair_kernel(PrefArgs a, PrefWs w) {
   }
 }
 
-template <class T>
-__global__ void __launch_bounds__(kRowThreads) pref_grad_kernel(PrefArgs a, PrefWs w) {
+// The gradient.  kT threads take a segment of 4 granules each of a row; segments (rows for
+// warps) are dealt to the blocks in descending order, so that the rows read last by
+// pref_stats_kernel, still in L2, come first.
+template <class T, int kT>
+__global__ void __launch_bounds__(kBlock) pref_grad_kernel(PrefArgs a, PrefWs w, int64_t segs) {
   wait_prior_grid();
   allow_next_grid();
-  for (int64_t t = blockIdx.x; t < a.logits.rows; t += gridDim.x) {
+  const int tid = threadIdx.x % kT;
+  constexpr int kItems = kBlock / kT, kSeg = kT * 4;
+  const int64_t items = a.logits.rows * segs;
+  for (int64_t it = (int64_t)blockIdx.x * kItems + threadIdx.x / kT; it < items;
+       it += (int64_t)gridDim.x * kItems) {
+    const int64_t rev = items - 1 - it;
+    const int64_t t = rev / segs, seg = rev - t * segs;
     const int64_t target = a.targets.at(t);
     const float g = w.coef[t];
+    const MaxSum ms{w.m[t], w.s[t]};
     const bool zero = target < 0 || target >= a.logits.cols || g == 0.0f;
-    row_grad(static_cast<const T*>(a.logits.p) + t * a.logits.ld,
-             static_cast<T*>(a.grad.p) + t * a.grad.ld, a.logits.cols, kLog2e,
-             {w.m[t], w.s[t]}, target, g, zero);
+    const Row<T> row(static_cast<const T*>(a.logits.p) + t * a.logits.ld, a.logits.cols);
+    const int64_t g1 = segs == 1 || seg == segs - 1 ? row.granules : (seg + 1) * kSeg;
+    row_grad(row, static_cast<T*>(a.grad.p) + t * a.grad.ld, seg * kSeg + tid, g1, kT, kLog2e, ms,
+             target, g, zero);
   }
 }
 
@@ -222,76 +360,401 @@ struct PolicyWs {
   float *loss, *kl, *clipped;  // per row
 };
 
-template <class T>
-__global__ void __launch_bounds__(kRowThreads) policy_kernel(PolicyArgs a, PolicyWs w) {
-  __shared__ float sg;
-  __shared__ int last;
-  wait_prior_grid();
-  allow_next_grid();
-  const float inv_t = 1.0f / a.temperature, scale2 = kLog2e * inv_t;
-  for (int64_t t = blockIdx.x; t < a.logits.rows; t += gridDim.x) {
-    const int64_t target = a.targets.at(t);
-    const bool bad = target >= a.logits.cols;
-    const bool masked = target < 0 || bad;
-    const T* x = static_cast<const T*>(a.logits.p) + t * a.logits.ld;
-    MaxSum r{0.0f, 1.0f};
-    if (!masked) r = row_max_sum(x, a.logits.cols, scale2);
-    if (threadIdx.x == 0) {
-      if (bad) set_status(w.ctrl, ST_BAD_INDEX);
-      const float wt = masked ? 0.0f : a.weights[t];
-      float lp = 0.0f, g = 0.0f, kl = 0.0f, l = 0.0f, clip = 0.0f;
-      if (!masked) lp = Elem<T>::get(x[target]) * inv_t - r.m / kLog2e - logf(r.s);
-      if (wt != 0.0f) {
-        const float adv = a.adv[t], ratio = expf(lp - a.old_logp[t]);
-        const float held = fminf(fmaxf(ratio, 1.0f - a.clip_low), 1.0f + a.clip_high);
-        const bool inside = adv >= 0.0f ? ratio <= 1.0f + a.clip_high : ratio >= 1.0f - a.clip_low;
-        l = -fminf(ratio * adv, held * adv);
-        g = inside ? -ratio * adv : 0.0f;
-        clip = inside ? 0.0f : 1.0f;
-        if (a.ref_logp) {
-          const float away = a.ref_logp[t] - lp;
-          kl = expm1f(away) - away;
-          l += a.kl * kl;
-          g -= a.kl * expm1f(away);
-        }
-      }
-      a.logp[t] = lp;
-      w.loss[t] = wt * l;
-      w.kl[t] = wt * kl;
-      w.clipped[t] = wt * clip;
-      sg = a.grad_scale * g * wt * inv_t;
-    }
-    __syncthreads();
-    const float g = sg;
-    const float wt = masked ? 0.0f : a.weights[t];
-    if (a.grad.p)
-      row_grad(x, static_cast<T*>(a.grad.p) + t * a.grad.ld, a.logits.cols, scale2, r, target, g,
-               masked || wt == 0.0f);
-    __syncthreads();
+// What the loss reads of a row beside its logits.
+struct RowInfo {
+  int64_t target;  // -1: masked
+  float xt, weight, old_logp, ref_logp, adv;
+};
+
+__device__ __forceinline__ bool load_info(const PolicyArgs& a, int64_t t, RowInfo& f) {
+  f.target = a.targets.at(t);
+  const bool bad = f.target >= a.logits.cols;
+  if (bad || f.target < 0) f.target = -1;
+  f.weight = a.weights[t];
+  f.old_logp = a.old_logp[t];
+  f.ref_logp = a.ref_logp ? a.ref_logp[t] : 0.0f;
+  f.adv = a.adv[t];
+  return bad;
+}
+
+// The row's loss terms (each times its weight) and g, the factor of its gradient by
+// logits / temperature.
+struct RowLoss {
+  float lp, loss, kl, clipped, g;
+};
+__device__ __forceinline__ RowLoss policy_row(const PolicyArgs& a, const RowInfo& f, MaxSum r,
+                                              float inv_t) {
+  RowLoss o{0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  if (f.target < 0) return o;
+  o.lp = log_prob(f.xt, r, inv_t);
+  if (f.weight == 0.0f) return o;
+  const float ratio = expf(o.lp - f.old_logp);
+  const float held = fminf(fmaxf(ratio, 1.0f - a.clip_low), 1.0f + a.clip_high);
+  const bool inside =
+      f.adv >= 0.0f ? ratio <= 1.0f + a.clip_high : ratio >= 1.0f - a.clip_low;
+  float l = -fminf(ratio * f.adv, held * f.adv), d = inside ? -ratio * f.adv : 0.0f;
+  if (a.ref_logp) {
+    const float away = f.ref_logp - o.lp, em = expm1f(away);
+    o.kl = f.weight * (em - away);
+    l += a.kl * (em - away);
+    d -= a.kl * em;
   }
+  o.loss = f.weight * l;
+  o.clipped = inside ? 0.0f : f.weight;
+  o.g = a.grad_scale * d * f.weight * inv_t;
+  return o;
+}
+
+__device__ __forceinline__ void put_row_loss(const PolicyArgs& a, const PolicyWs& w, int64_t t,
+                                             const RowLoss& o) {
+  a.logp[t] = o.lp;
+  w.loss[t] = o.loss;
+  w.kl[t] = o.kl;
+  w.clipped[t] = o.clipped;
+}
+
+// The last of `blocks` blocks to come here adds the rows' terms in a fixed order.  Called
+// by every thread of the block's first kBlock.
+__device__ void policy_sums(const PolicyArgs& a, const PolicyWs& w, unsigned blocks, int bar) {
+  __shared__ int last;
+  __shared__ double red[3][kBlock / 32];
   __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) last = atomicAdd(&w.ctrl->loss_done, 1u) == gridDim.x - 1;
-  __syncthreads();
+  asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(kBlock) : "memory");
+  if (threadIdx.x == 0) last = atomicAdd(&w.ctrl->loss_done, 1u) == blocks - 1;
+  asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(kBlock) : "memory");
   if (!last) return;
   __threadfence();
-  __shared__ double red[3][kRowThreads];
   double s[3] = {0, 0, 0};
-  for (int64_t t = threadIdx.x; t < a.logits.rows; t += kRowThreads) {
+  for (int64_t t = threadIdx.x; t < a.logits.rows; t += kBlock) {
     s[0] += __ldcg(&w.loss[t]);
     s[1] += __ldcg(&w.kl[t]);
     s[2] += __ldcg(&w.clipped[t]);
   }
-  for (int e = 0; e < 3; ++e) red[e][threadIdx.x] = s[e];
-  for (int h = kRowThreads / 2; h > 0; h /= 2) {
-    __syncthreads();
-    if (threadIdx.x < h)
-      for (int e = 0; e < 3; ++e) red[e][threadIdx.x] += red[e][threadIdx.x + h];
+#pragma unroll
+  for (int e = 0; e < 3; ++e) {
+#pragma unroll
+    for (int h = 16; h > 0; h /= 2) s[e] += __shfl_xor_sync(0xffffffffu, s[e], h);
+    if ((threadIdx.x & 31) == 0) red[e][threadIdx.x >> 5] = s[e];
   }
+  asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(kBlock) : "memory");
+  if (threadIdx.x < 3) {
+    double v = 0.0;
+    for (int i = 0; i < kBlock / 32; ++i) v += red[threadIdx.x][i];
+    a.stats[threadIdx.x] = (float)v;
+  }
+  if (threadIdx.x == 0) w.ctrl->loss_done = 0;
+}
+
+// Rows too long to be held on chip, and rows short enough for a warp: the row is read,
+// then read again (from L2 or L1) for its gradient.  kT threads per row.
+template <class T, int kT>
+__global__ void __launch_bounds__(kBlock) policy_reread_kernel(PolicyArgs a, PolicyWs w) {
+  wait_prior_grid();
+  allow_next_grid();
+  const int tid = threadIdx.x % kT;
+  constexpr int kRows = kBlock / kT;
+  const float inv_t = 1.0f / a.temperature, scale = kLog2e * inv_t;
+  for (int64_t t = (int64_t)blockIdx.x * kRows + threadIdx.x / kT; t < a.logits.rows;
+       t += (int64_t)gridDim.x * kRows) {
+    RowInfo f;
+    if (load_info(a, t, f) && tid == 0) set_status(w.ctrl, ST_BAD_INDEX);
+    const Row<T> row(static_cast<const T*>(a.logits.p) + t * a.logits.ld, a.logits.cols);
+    MaxSum r{0.0f, 1.0f};
+    f.xt = 0.0f;
+    if (f.target >= 0) {
+      f.xt = Elem<T>::get(row.x[f.target]);
+      r = row_max_sum<T, kT>(row, tid, scale);
+    }
+    const RowLoss o = policy_row(a, f, r, inv_t);
+    if (tid == 0) put_row_loss(a, w, t, o);
+    if (a.grad.p)
+      row_grad(row, static_cast<T*>(a.grad.p) + t * a.grad.ld, (int64_t)tid, row.granules, kT,
+               scale, r, f.target, o.g, f.target < 0 || f.weight == 0.0f);
+  }
+  policy_sums(a, w, gridDim.x, 0);
+}
+
+// Rows held on chip.  A cluster of C CTAs takes a row, each CTA a slice of up to
+// kBlock * kQ granules, kQ per thread.  A producer warp copies the slices of the next rows
+// into a ring of three stages with bulk copies and passes the row's scalars along; the
+// other warps turn a stage into exponentials against the thread's own maximum, kept in
+// registers (so the stage is free again before the row's sum is known), exchange one
+// (maximum, sum) pair per warp with the whole cluster through distributed shared memory,
+// and scale their exponentials into the gradient.  One read and one write per element,
+// one exponential, and one exchange per row.
+constexpr int kStages = 3;
+constexpr int kConsumers = kBlock, kRingThreads = kBlock + 32;
+constexpr int kWarps = kConsumers / 32;
+constexpr int kMaxCluster = 8;
+constexpr uint64_t kTimeoutNs = 1000000000ull;
+
+struct RingShared {
+  uint64_t full[kStages], empty[kStages], red[2];
+  uint64_t pair[2][kMaxCluster * kWarps];  // (max, sum) of every warp of the cluster
+  RowInfo info[kStages];
+  volatile uint32_t abort;
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+               ::: "memory");
+}
+// Writes v to the same shared address of CTA `rank` of the cluster and counts its 8 bytes
+// on that CTA's barrier.
+__device__ __forceinline__ void send_pair(uint64_t* dst, uint64_t* bar, uint32_t rank, uint64_t v) {
+  asm volatile(
+      "{\n\t.reg .b32 d, b;\n\t"
+      "mapa.shared::cluster.u32 d, %0, %2;\n\t"
+      "mapa.shared::cluster.u32 b, %1, %2;\n\t"
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b64 [d], %3, [b];\n\t}" ::"r"(
+          smem_u32(dst)),
+      "r"(smem_u32(bar)), "r"(rank), "l"(v)
+      : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// Bounded wait; false if the phase does not complete in time or the CTA gave up.
+template <bool kCluster>
+__device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity, RingShared* sh,
+                                          Ctrl* ctrl) {
+  if (kCluster ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    if (kCluster ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+    if (sh->abort) return false;
+    if (globaltimer_ns() - t0 > kTimeoutNs) {
+      sh->abort = 1;
+      atomicOr(&ctrl->status, ST_TIMEOUT);
+      return false;
+    }
+  }
+}
+
+template <class T, int kQ>
+constexpr size_t ring_bytes() {
+  return (size_t)kStages * kBlock * kQ * 16 + sizeof(RingShared) + 16;
+}
+
+// Blocks per SM: as many as the stages leave room for, and the registers that hold a row.
+template <class T, int kQ>
+constexpr int ring_blocks() {
+  return kQ * 16 / sizeof(T) <= 16 ? 3 : sizeof(T) == 2 ? 2 : 1;
+}
+
+template <class T, int kQ>
+__global__ void __launch_bounds__(kRingThreads, ring_blocks<T, kQ>())
+    policy_kernel(PolicyArgs a, PolicyWs w, int C) {
+  constexpr int kV = Row<T>::kV;
+  extern __shared__ __align__(16) uint8_t ring[];
+  RingShared* sh = reinterpret_cast<RingShared*>(ring + (size_t)kStages * kBlock * kQ * 16);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = C > 1 ? cluster_rank() : 0u;
+  const int64_t cluster = blockIdx.x / C, clusters = gridDim.x / C;
   if (threadIdx.x == 0) {
-    for (int e = 0; e < 3; ++e) a.stats[e] = (float)red[e][0];
-    w.ctrl->loss_done = 0;
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&sh->full[i], 1);
+      mbar_init(&sh->empty[i], kWarps);
+    }
+    mbar_init(&sh->red[0], 1);
+    mbar_init(&sh->red[1], 1);
+    sh->abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  __syncthreads();
+  cluster_sync();
+  wait_prior_grid();
+  allow_next_grid();
+  const float inv_t = 1.0f / a.temperature, scale = kLog2e * inv_t;
+  const T* logits = static_cast<const T*>(a.logits.p);
+
+  if (warp == kWarps) {
+    // ---------------------------------------------------------------- producer warp
+    int stage = 0;
+    uint32_t phase = 0, issued = 0, last_par = 0;
+    bool ok = true;
+    for (int64_t t0 = cluster; t0 < a.logits.rows && ok; t0 += 32 * clusters) {
+      // the scalars of the next 32 rows, one row per lane
+      RowInfo mine{-1, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+      const int64_t tl = t0 + lane * clusters;
+      if (tl < a.logits.rows) {
+        if (load_info(a, tl, mine) && rank == 0) set_status(w.ctrl, ST_BAD_INDEX);
+        if (mine.target >= 0) mine.xt = Elem<T>::get(logits[tl * a.logits.ld + mine.target]);
+      }
+      for (int i = 0; i < 32; ++i) {
+        const int64_t t = t0 + i * clusters;
+        if (t >= a.logits.rows) break;
+        ok = __shfl_sync(0xffffffffu,
+                         lane == 0 ? (int)ring_wait<false>(&sh->empty[stage], phase ^ 1u, sh,
+                                                           w.ctrl) : 0, 0) != 0;
+        if (!ok) break;
+        const int64_t target = __shfl_sync(0xffffffffu, mine.target, i);
+        if (lane == i) sh->info[stage] = mine;
+        uint32_t bytes = 0;
+        int64_t b0 = 0, c0 = 0;
+        const Row<T> row(logits + t * a.logits.ld, a.logits.cols);
+        T* buf = reinterpret_cast<T*>(ring + (size_t)stage * kBlock * kQ * 16);
+        if (target >= 0) {
+          const int64_t per = (row.granules + C - 1) / C;
+          c0 = rank * per;
+          const int64_t c1 = c0 + per < row.granules ? c0 + per : row.granules;
+          if (c0 < c1) {
+            // granules shared with other rows: their elements one by one (lanes 0-15)
+            b0 = row.whole(c0) ? c0 : c0 + 1;
+            int64_t b1 = c1 > b0 && !row.whole(c1 - 1) ? c1 - 1 : c1;
+            if (b1 < b0) b1 = b0;
+            const int64_t eg = lane < 8 ? c0 : c1 - 1;
+            const int e = lane & 7;
+            if (lane < 16 && e < kV && (lane < 8 ? b0 > c0 : b1 < c1 && b1 >= b0)) {
+              const int64_t el = row.first(eg) + e;
+              if (el >= 0 && el < row.n) buf[(eg - c0) * kV + e] = row.x[el];
+            }
+            bytes = (uint32_t)((b1 - b0) * 16);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) {
+          if (bytes) {
+            mbar_expect_tx(&sh->full[stage], bytes);
+            bulk_load(buf + (b0 - c0) * kV, row.x + row.first(b0), bytes, &sh->full[stage]);
+            issued |= 1u << stage;
+            last_par = (last_par & ~(1u << stage)) | (phase << stage);
+          } else {  // (an earlier copy into this stage has landed: its row was consumed)
+            mbar_arrive(&sh->full[stage]);
+            issued &= ~(1u << stage);
+          }
+        }
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (lane == 0)  // every copy has landed before the CTA may exit
+      for (int st = 0; st < kStages; ++st)
+        if (issued & (1u << st)) {
+          const uint64_t t0 = globaltimer_ns();
+          while (!mbar_try_wait(&sh->full[st], (last_par >> st) & 1u) &&
+                 globaltimer_ns() - t0 < kTimeoutNs) {
+          }
+        }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- the other warps
+    int stage = 0;
+    uint32_t phase = 0, count = 0;
+    for (int64_t t = cluster; t < a.logits.rows; t += clusters) {
+      if (!__all_sync(0xffffffffu, ring_wait<false>(&sh->full[stage], phase, sh, w.ctrl))) break;
+      const RowInfo f = sh->info[stage];
+      const Row<T> row(logits + t * a.logits.ld, a.logits.cols);
+      const int64_t per = (row.granules + C - 1) / C, c0 = rank * per;
+      const int n = (int)(c0 + per < row.granules ? per : c0 < row.granules ? row.granules - c0 : 0);
+      float e[kQ][kV];
+      MaxSum mine{-INFINITY, 0.0f}, r{0.0f, 1.0f};
+      if (f.target >= 0) {
+        const Pack<T, kV>* buf =
+            reinterpret_cast<const Pack<T, kV>*>(ring + (size_t)stage * kBlock * kQ * 16);
+#pragma unroll
+        for (int q = 0; q < kQ; ++q) {
+          const int i = threadIdx.x + q * kBlock;
+          if (i < n) {
+            const Pack<T, kV> p = buf[i];
+#pragma unroll
+            for (int j = 0; j < kV; ++j) e[q][j] = Elem<T>::get(p.v[j]);
+            if (!row.whole(c0 + i)) {
+              const int64_t el = row.first(c0 + i);
+#pragma unroll
+              for (int j = 0; j < kV; ++j)
+                if (el + j < 0 || el + j >= row.n) e[q][j] = -INFINITY;
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < kV; ++j) e[q][j] = -INFINITY;
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->empty[stage]);
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+      if (f.target >= 0) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < kQ; ++q)
+#pragma unroll
+          for (int j = 0; j < kV; ++j) top = fmaxf(top, e[q][j]);
+        const float base = top == -INFINITY ? 0.0f : top;
+        float s[4] = {};
+#pragma unroll
+        for (int q = 0; q < kQ; ++q)
+#pragma unroll
+          for (int j = 0; j < kV; ++j) {
+            e[q][j] = fast_exp2((e[q][j] - base) * scale);
+            s[j & 3] += e[q][j];
+          }
+        mine = {top, (s[0] + s[1]) + (s[2] + s[3])};
+        const MaxSum wp = join_lanes<32>(mine, scale);
+        uint64_t* slots = sh->pair[count & 1];
+        uint64_t* bar = &sh->red[count & 1];
+        if (threadIdx.x == 0) mbar_expect_tx(bar, (uint32_t)(C * kWarps * 8));
+        if (lane < C)
+          send_pair(slots + rank * kWarps + warp, bar, lane,
+                    (uint64_t)__float_as_uint(wp.s) << 32 | __float_as_uint(wp.m));
+        if (!__all_sync(0xffffffffu, ring_wait<true>(bar, (count >> 1) & 1u, sh, w.ctrl))) break;
+        ++count;
+        MaxSum x{-INFINITY, 0.0f}, y{-INFINITY, 0.0f};
+        if (lane < C * kWarps) {
+          const uint64_t v = slots[lane];
+          x = {__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32))};
+        }
+        if (lane + 32 < C * kWarps) {
+          const uint64_t v = slots[lane + 32];
+          y = {__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32))};
+        }
+        r = join_lanes<32>(join(x, y, scale), scale);
+      }
+      const RowLoss o = policy_row(a, f, r, inv_t);
+      if (rank == 0 && threadIdx.x == 0) put_row_loss(a, w, t, o);
+      if (!a.grad.p) continue;
+      T* out = static_cast<T*>(a.grad.p) + t * a.grad.ld;
+      const bool al = same_phase(row.x, out);
+      const bool zero = f.target < 0 || f.weight == 0.0f;
+      const float k = zero ? 0.0f : -o.g / r.s * rescale(mine.m, r.m, scale);
+#pragma unroll
+      for (int q = 0; q < kQ; ++q) {
+        const int i = threadIdx.x + q * kBlock;
+        if (i >= n) break;
+        float v[kV];
+#pragma unroll
+        for (int j = 0; j < kV; ++j) v[j] = zero ? 0.0f : k * e[q][j];
+        put_granule(row, out, al, c0 + i, v);
+      }
+      if (!zero) {  // the thread that stored the target's granule sets the target
+        const int64_t i = (f.target + row.shift) / kV - c0;
+        if (i >= 0 && i < n && (int)(i % kBlock) == (int)threadIdx.x)
+          out[f.target] = Elem<T>::put(target_grad(o.g, f.xt, r, scale));
+      }
+    }
+    if (rank == 0) policy_sums(a, w, (unsigned)clusters, 1);
+  }
+  __syncwarp();
+  cluster_sync();  // no CTA leaves while another may still write to its shared memory
 }
 
 template <class... P, class... A>
@@ -306,21 +769,75 @@ cudaError_t launch(Ctx& c, unsigned grid, unsigned block, void (*fn)(P...), A...
   return cudaLaunchKernelEx(&cfg, fn, P(args)...);
 }
 
-template <class T>
+unsigned blocks_for(int64_t items, int64_t most) {
+  return (unsigned)(items < 1 ? 1 : items < most ? items : most);
+}
+
+template <class T, int kT>
 cudaError_t pref_typed(const PrefArgs& p, const PrefWs& w, Ctx& c) {
-  const unsigned grid = (unsigned)(p.logits.rows < 65535 ? p.logits.rows : 65535);
+  constexpr int kV = 16 / sizeof(T), kItems = kBlock / kT;
+  const int64_t rows = p.logits.rows;
   cudaError_t e = cudaSuccess;
-  if (grid) e = launch(c, grid, kRowThreads, pref_stats_kernel<T>, p, w);
-  if (e == cudaSuccess) e = launch(c, (unsigned)p.pairs, 256, pref_pair_kernel, p, w);
-  if (e == cudaSuccess && grid && p.grad.p)
-    e = launch(c, grid, kRowThreads, pref_grad_kernel<T>, p, w);
+  if (rows)
+    e = launch(c, blocks_for((rows + kItems - 1) / kItems, 1 << 20), kBlock,
+               pref_stats_kernel<T, kT>, p, w);
+  if (e == cudaSuccess) e = launch(c, (unsigned)p.pairs, kBlock, pref_pair_kernel, p, w);
+  if (e == cudaSuccess && rows && p.grad.p) {
+    // (one granule more than cols / kV for rows that do not start on one)
+    int64_t segs = ((p.logits.cols + kV - 1) / kV + 1 + kT * 4 - 1) / (kT * 4);
+    if (kT == 32) segs = 1;
+    e = launch(c, blocks_for((rows * segs + kItems - 1) / kItems, 1 << 20), kBlock,
+               pref_grad_kernel<T, kT>, p, w, segs);
+  }
   return e;
+}
+template <class T>
+cudaError_t pref_by_width(const PrefArgs& p, const PrefWs& w, Ctx& c) {
+  return p.logits.cols <= kWarpCols ? pref_typed<T, 32>(p, w, c) : pref_typed<T, kBlock>(p, w, c);
+}
+
+template <class T, int kQ>
+cudaError_t policy_ring(const PolicyArgs& p, const PolicyWs& w, int C, Ctx& c) {
+  const auto fn = policy_kernel<T, kQ>;
+  const size_t smem = ring_bytes<T, kQ>();
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)C;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(kRingThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = c.stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3((unsigned)C);
+  int fit = 0;  // clusters that fit the GPU at once: one wave, each taking every fit-th row
+  e = cudaOccupancyMaxActiveClusters(&fit, fn, &cfg);
+  if (e != cudaSuccess) return e;
+  if (fit < 1) return cudaErrorInvalidConfiguration;
+  cfg.gridDim = dim3((unsigned)C * blocks_for(p.logits.rows, fit));
+  add_pdl_attr(c, cfg, attr);
+  ++c.launches;
+  return cudaLaunchKernelEx(&cfg, fn, p, w, C);
 }
 
 template <class T>
 cudaError_t policy_typed(const PolicyArgs& p, const PolicyWs& w, Ctx& c) {
-  const int64_t rows = p.logits.rows > 0 ? p.logits.rows : 1;
-  return launch(c, (unsigned)(rows < 65535 ? rows : 65535), kRowThreads, policy_kernel<T>, p, w);
+  constexpr int kV = 16 / sizeof(T);
+  constexpr int kSmall = 16 / kV, kLarge = 64 / kV;  // 16 or 64 elements per thread
+  const int64_t rows = p.logits.rows;
+  const int64_t granules = (p.logits.cols + kV - 1) / kV + 1;  // at most, at any alignment
+  if (p.logits.cols <= kWarpCols || rows == 0)
+    return launch(c, blocks_for((rows + 7) / 8, 1 << 20), kBlock, policy_reread_kernel<T, 32>, p,
+                  w);
+  for (int C = 1; C <= kMaxCluster; C *= 2)
+    if (granules <= (int64_t)C * kBlock * kSmall && (C == 1 || rows * C <= 8 * c.num_sms))
+      return policy_ring<T, kSmall>(p, w, C, c);
+  for (int C = 1; C <= kMaxCluster; C *= 2)
+    if (granules <= (int64_t)C * kBlock * kLarge) return policy_ring<T, kLarge>(p, w, C, c);
+  return launch(c, blocks_for(rows, 1 << 20), kBlock, policy_reread_kernel<T, kBlock>, p, w);
 }
 
 }  // namespace
@@ -338,9 +855,9 @@ cudaError_t launch_preference(const PrefArgs& p, void* ws, Ctx& c) {
   auto f = [&](size_t o) { return reinterpret_cast<float*>(b + o); };
   const PrefWs w{reinterpret_cast<Ctrl*>(b), f(L.off_m), f(L.off_s), f(L.off_lp), f(L.off_coef),
                  reinterpret_cast<double*>(b + L.off_loss)};
-  if (p.logits.dtype == CASGD_F32) return pref_typed<float>(p, w, c);
-  if (p.logits.dtype == CASGD_BF16) return pref_typed<__nv_bfloat16>(p, w, c);
-  return pref_typed<__half>(p, w, c);
+  if (p.logits.dtype == CASGD_F32) return pref_by_width<float>(p, w, c);
+  if (p.logits.dtype == CASGD_BF16) return pref_by_width<__nv_bfloat16>(p, w, c);
+  return pref_by_width<__half>(p, w, c);
 }
 
 cudaError_t launch_policy(const PolicyArgs& p, void* ws, Ctx& c) {

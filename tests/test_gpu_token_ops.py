@@ -647,6 +647,39 @@ def test_policy_rows(gpu_lib, rows):
     check_policy(gpu_lib, policy_inputs(rows, 320, "bf16", seed=rows), "bf16")
 
 
+# many rows for each group of threads that takes them in turn, masked ones between
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("rows,vocab", [(3000, 2100), (2500, 4097), (1500, 9001), (700, 33000),
+                                        (500, 128000)])
+def test_policy_many_rows(gpu_lib, dt, rows, vocab):
+    i = policy_inputs(rows, vocab, dt, seed=rows, masked=0.3)
+    ws, out = gpu_lib.policy_workspace(rows), gpu_lib.PolicyOut.alloc(rows)
+    grad = torch.empty_like(i["x"])
+    for _ in range(3):
+        t0 = torch.cuda.Event(enable_timing=True)
+        t1 = torch.cuda.Event(enable_timing=True)
+        t0.record()
+        gpu_lib.policy_loss(i["x"], i["t"], i["w"], i["old"], i["adv"], grad, out, ws,
+                            ref_logp=i["ref"], kl=0.1, clip_low=0.2, clip_high=0.3)
+        t1.record()
+    assert gpu_lib.get_status(ws) == 0
+    assert t0.elapsed_time(t1) < 200                    # no wait ran into its bound (1 s)
+    stats, logp, first = out.stats.clone(), out.logp.clone(), grad.clone()
+    lp, p, keep, at, eps = row_reference(i["x"], i["t"])
+    close(logp, lp, eps + 4 * E32 * (lp.abs() + 1))
+    # rows of the gradient sum to zero up to their rounding, and none is left unwritten
+    assert torch.isfinite(first).all() and (first[~keep] == 0).all()
+    mag = first.double().abs().sum(1)
+    bound = (ULP[dt] + eps + 8 * E32) * mag + vocab * TINY[dt]
+    assert (first.double().sum(1).abs() <= bound).all()
+    again, _ = run_policy(gpu_lib, i, grad.zero_(), kl=0.1, clip_low=0.2, clip_high=0.3)
+    assert torch.equal(grad, first) and torch.equal(again.logp, logp)   # the same bits
+    assert torch.equal(again.stats, stats)
+    run_policy(gpu_lib, i, i["x"], kl=0.1, clip_low=0.2, clip_high=0.3)        # in place
+    assert torch.equal(i["x"], first)
+    assert torch.isfinite(stats).all()
+
+
 @pytest.mark.parametrize("dt", ["f16", "f32"])
 @pytest.mark.parametrize("vocab,pad,shift", [(96, 8, 0), (97, 0, 0), (101, 3, 1), (12345, 2, 5),
                                              (70003, 1, 3)])
