@@ -88,16 +88,21 @@ cudaError_t embed_from(const Mat& t, Ids ids, float s, int64_t pad, const Mat& o
 
 // ------------------------------------------------------------------ sort by token
 // Stable radix sort of (token, position) pairs, least significant digit first.  A token
-// that is dropped (padding, or out of range) sorts last, with the key `vocab`.  Tiles of
-// kTile pairs; per pass a tile's scatter base of a digit is the count of smaller digits
-// everywhere plus that of the same digit in the tiles before it, summed by the tile
-// itself from the per-tile counts (a few hundred KB from L2), so a pass is one launch:
-// the scatter of pass p adds each pair to the counts of pass p+1 at its destination.
-constexpr int kSortThreads = 256;
+// that is dropped (padding, or out of range) sorts last, with the key `vocab`.
+//
+// Up to kMaxCluster * kTile tokens: one launch.  A cluster sorts, a tile of kTile pairs
+// per CTA; per pass the CTAs read one another's digit counts through distributed shared
+// memory, scatter through global memory (L2) and meet at a cluster barrier.  The other
+// CTAs of the launch clear the gradient meanwhile, which hides the sort wherever the
+// table takes longer to clear.  More tokens: one launch that counts the first digit (and
+// clears), then one per pass.  There a tile's scatter base comes from the per-tile counts
+// in global memory, which the scatter of a pass keeps for the next pass's tiles.
+constexpr int kSortThreads = 1024;
 constexpr int kSortItems = 8;  // per thread
 constexpr int kTile = kSortThreads * kSortItems;
+constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxRadix = 512;
-constexpr int kMaxPasses = 4;
+constexpr int kMaxCluster = 8;
 
 struct SortPlan {
   int passes, bits;  // digits of `bits` bits
@@ -114,8 +119,7 @@ SortPlan sort_plan(int64_t vocab) {
 
 struct GradLayout {
   int64_t tiles, chunks, chunk;
-  size_t off_count, off_key[2], off_pos[2], off_seen, off_part, off_owner, total;
-  size_t count_bytes, seen_bytes;
+  size_t off_count, off_key[2], off_pos[2], off_part, off_owner, total;
 };
 
 GradLayout grad_layout(int64_t rows, int64_t vocab, int64_t dim) {
@@ -123,18 +127,14 @@ GradLayout grad_layout(int64_t rows, int64_t vocab, int64_t dim) {
   L.tiles = rows > 0 ? (rows + kTile - 1) / kTile : 1;
   // Chunk length: enough chunks to fill the GPU, few enough partial sums for long lists.
   L.chunk = 8;
-  while (L.chunk < 64 && rows / L.chunk > 2048) L.chunk *= 2;
+  while (L.chunk < 64 && rows / L.chunk > 4096) L.chunk *= 2;
   L.chunks = (rows + L.chunk - 1) / L.chunk;
   const SortPlan p = sort_plan(vocab);
   size_t o = align_up(sizeof(Ctrl));
-  L.off_count = o;
-  L.count_bytes = align_up((size_t)p.passes * L.tiles * p.radix() * 4);
-  o += L.count_bytes;
-  L.off_seen = o;
-  L.seen_bytes = align_up((size_t)(vocab / 32 + 1) * 4);
-  o += L.seen_bytes;
-  L.off_owner = o;  // word 0: how many; then the first chunk of every run that crosses
-  o += align_up((size_t)(L.chunks + 1) * 4);
+  L.off_count = o;  // per-tile counts, for lists that one cluster does not sort
+  if (L.tiles > kMaxCluster) o += align_up((size_t)p.passes * L.tiles * p.radix() * 4);
+  L.off_owner = o;  // word 0: how many; then (first chunk, end chunk) of every run that
+  o += align_up((size_t)(2 * L.chunks + 2) * 4);  // crosses a chunk border
   for (int i = 0; i < 2; ++i) {
     L.off_key[i] = o;
     o += align_up((size_t)rows * 4);
@@ -152,156 +152,289 @@ struct SortArgs {
   int64_t rows, vocab, padding_id, tiles;
   int bits, passes;
   uint32_t* count;  // [pass][tile][digit]
-  uint32_t* seen;   // one bit per table row that receives a gradient
+  uint32_t* key[2];
+  uint32_t* pos[2];
   uint32_t* owner;
-  int64_t seen_words;
   Ctrl* ctrl;
+};
+
+struct ClearArgs {  // the gradient as rows of 16-byte units, or of elements
+  void* p;
+  int64_t rows, row_bytes, pitch_bytes;
+  int wide;
 };
 
 __device__ __forceinline__ uint32_t sort_key(const SortArgs& a, int64_t i, bool& bad) {
   const int64_t id = a.ids.at(i);
-  bad = id != a.padding_id && (id < 0 || id >= a.vocab);
-  return id == a.padding_id || bad ? (uint32_t)a.vocab : (uint32_t)id;
+  const bool out = id < 0 || id >= a.vocab;
+  bad |= id != a.padding_id && out;
+  return id == a.padding_id || out ? (uint32_t)a.vocab : (uint32_t)id;
 }
 
-// Clears what the later launches add to, and counts the first digit of every tile.
-__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortArgs a) {
-  __shared__ uint32_t cnt[kMaxRadix];
-  wait_prior_grid();
-  allow_next_grid();
-  const int radix = 1 << a.bits;
-  const int64_t gid = (int64_t)blockIdx.x * kSortThreads + threadIdx.x;
-  const int64_t gn = (int64_t)gridDim.x * kSortThreads;
-  for (int64_t i = gid; i < a.seen_words; i += gn) a.seen[i] = 0;
-  for (int64_t i = gid; i < (int64_t)(a.passes - 1) * a.tiles * radix; i += gn)
-    a.count[a.tiles * radix + i] = 0;
-  if (gid == 0) a.owner[0] = 0;
-  for (int d = threadIdx.x; d < radix; d += kSortThreads) cnt[d] = 0;
-  __syncthreads();
-  const int64_t t0 = (int64_t)blockIdx.x * kTile;
-  bool any_bad = false;
-  for (int j = 0; j < kSortItems; ++j) {
-    const int64_t i = t0 + j * kSortThreads + threadIdx.x;
-    if (i >= a.rows) break;
-    bool bad;
-    const uint32_t k = sort_key(a, i, bad);
-    any_bad |= bad;
-    atomicAdd(&cnt[k & (radix - 1)], 1u);
+// Zeros to the whole gradient: a warp per row.
+__device__ void clear_rows(const ClearArgs& c, int64_t block, int64_t blocks) {
+  const int64_t warp = block * kSortWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  for (int64_t r = warp; r < c.rows; r += blocks * kSortWarps) {
+    char* row = static_cast<char*>(c.p) + r * c.pitch_bytes;
+    if (c.wide) {
+      for (int64_t i = lane * 16; i < c.row_bytes; i += 512)
+        *reinterpret_cast<uint4*>(row + i) = make_uint4(0, 0, 0, 0);
+    } else if (c.row_bytes % 4 == 0 && c.pitch_bytes % 4 == 0 &&
+               reinterpret_cast<uintptr_t>(c.p) % 4 == 0) {
+      for (int64_t i = lane * 4; i < c.row_bytes; i += 128)
+        *reinterpret_cast<uint32_t*>(row + i) = 0u;
+    } else {
+      for (int64_t i = lane * 2; i < c.row_bytes; i += 64)
+        *reinterpret_cast<uint16_t*>(row + i) = 0;
+    }
   }
-  if (any_bad) set_status(a.ctrl, ST_BAD_INDEX);
-  __syncthreads();
-  for (int d = threadIdx.x; d < radix; d += kSortThreads)
-    a.count[(int64_t)blockIdx.x * radix + d] = cnt[d];
 }
 
-// One pass.  A warp owns kSortItems * 32 consecutive pairs; equal digits within a warp
-// are ranked by lane (match), earlier items of the warp by its own counters, earlier
-// warps by a sum over the counters.
-__global__ void __launch_bounds__(kSortThreads)
-    sort_scatter_kernel(SortArgs a, int pass, const uint32_t* key_in, const uint32_t* pos_in,
-                        uint32_t* key_out, uint32_t* pos_out) {
-  constexpr int kWarps = kSortThreads / 32;
-  __shared__ uint32_t cnt[kWarps][kMaxRadix];
-  __shared__ uint32_t base[kMaxRadix];
-  __shared__ uint32_t wsum[kWarps];
-  wait_prior_grid();
-  allow_next_grid();
-  const int radix = 1 << a.bits, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t tile = blockIdx.x;
-  for (int d = threadIdx.x; d < radix; d += kSortThreads)
-    for (int w = 0; w < kWarps; ++w) cnt[w][d] = 0;
-  // counts: of this digit in earlier tiles, and of every tile
-  const uint32_t* cp = a.count + (int64_t)pass * a.tiles * radix;
-  uint32_t before[2] = {0, 0}, total[2] = {0, 0};
+// A tile's digits: counted per warp in cnt[warp][digit], each pair's rank among the equal
+// digits of its warp in rank[].  A warp owns kSortItems * 32 consecutive pairs; equal
+// digits of a round are ranked by lane, earlier rounds by the counter.
+struct TileRanks {
+  uint32_t key[kSortItems], pos[kSortItems];
+  uint16_t rank[kSortItems];
+};
+__device__ __forceinline__ void rank_tile(TileRanks& t, int64_t w0, int64_t rows, int shift,
+                                          int radix, uint16_t* cnt) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int d = 2 * threadIdx.x + h;
-    if (d < radix)
-      for (int64_t t = 0; t < a.tiles; ++t) {
-        const uint32_t v = cp[t * radix + d];
-        total[h] += v;
-        if (t < tile) before[h] += v;
-      }
+  for (int j = 0; j < kSortItems; ++j) {
+    const bool in = w0 + j * 32 + lane < rows;
+    const uint32_t d = in ? (t.key[j] >> shift) & (radix - 1) : 0xffffffffu;
+    const uint32_t same = __match_any_sync(0xffffffffu, d);
+    const int first = __ffs(same) - 1;
+    uint32_t old = 0;
+    if (in && lane == first) {
+      old = cnt[d];
+      cnt[d] = (uint16_t)(old + __popc(same));
+    }
+    old = __shfl_sync(0xffffffffu, old, first);
+    t.rank[j] = (uint16_t)(old + __popc(same & ((1u << lane) - 1u)));
+    __syncwarp();
   }
-  // exclusive sum of the totals over the digits
-  uint32_t run = total[0] + total[1];
-  uint32_t inc = run;
+}
+
+struct SortShared {
+  uint16_t cnt[kSortWarps][kMaxRadix];  // per warp, then the warps before it
+  uint32_t total[2][kMaxRadix];         // of the tile (alternating per pass: peers read it)
+  uint32_t base[kMaxRadix];
+  uint32_t wsum[kMaxRadix / 32];
+};
+
+// From cnt: the tile's count of each digit into total, and each warp's into the count of
+// the warps before it.
+__device__ __forceinline__ void sum_warps(SortShared& s, int radix, uint32_t* total) {
+  for (int d = threadIdx.x; d < radix; d += kSortThreads) {
+    uint32_t sum = 0;
+#pragma unroll 8
+    for (int w = 0; w < kSortWarps; ++w) {
+      const uint32_t v = s.cnt[w][d];
+      s.cnt[w][d] = (uint16_t)sum;
+      sum += v;
+    }
+    total[d] = sum;
+  }
+}
+
+// base[d] = pairs of smaller digits everywhere + before (this digit's, of earlier tiles).
+// Digit threadIdx.x; all: the count of this digit everywhere.
+__device__ __forceinline__ void scan_digits(SortShared& s, int radix, uint32_t all,
+                                            uint32_t before) {
+  const int d = threadIdx.x, warp = d >> 5, lane = d & 31;
+  uint32_t inc = all;
 #pragma unroll
   for (int o = 1; o < 32; o *= 2) {
     const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += v;
   }
-  if (lane == 31) wsum[warp] = inc;
+  if (d < kMaxRadix && lane == 31) s.wsum[warp] = inc;
   __syncthreads();
-  uint32_t pre = inc - run;
-  for (int w = 0; w < warp; ++w) pre += wsum[w];
-  if (2 * threadIdx.x < radix) base[2 * threadIdx.x] = pre + before[0];
-  if (2 * threadIdx.x + 1 < radix) base[2 * threadIdx.x + 1] = pre + total[0] + before[1];
+  if (d < radix) {
+    uint32_t pre = inc - all + before;
+    for (int w = 0; w < warp; ++w) pre += s.wsum[w];
+    s.base[d] = pre;
+  }
+  __syncthreads();
+}
 
-  const int64_t w0 = tile * kTile + (int64_t)warp * kSortItems * 32;
-  uint32_t key[kSortItems], pos[kSortItems], rank[kSortItems];
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+               ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_u32(const uint32_t* p, uint32_t rank) {
+  uint32_t v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\t"
+      "ld.shared::cluster.u32 %0, [a];\n\t}"
+      : "=r"(v)
+      : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank)
+      : "memory");
+  return v;
+}
+
+// The whole sort by the first cluster of the launch; the other clusters clear.
+__global__ void __launch_bounds__(kSortThreads) sort_kernel(SortArgs a, ClearArgs c) {
+  extern __shared__ __align__(16) uint8_t sort_smem[];
+  SortShared& s = *reinterpret_cast<SortShared*>(sort_smem);
+  wait_prior_grid();
+  allow_next_grid();
+  const int C = (int)a.tiles;
+  if ((int)blockIdx.x >= C) {
+    clear_rows(c, blockIdx.x - C, gridDim.x - C);
+    return;  // (whole clusters: nothing here meets a cluster barrier)
+  }
+  const int radix = 1 << a.bits, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t w0 = (int64_t)blockIdx.x * kTile + (int64_t)warp * kSortItems * 32;
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.owner[0] = 0;
+  TileRanks t;
+  bool bad = false;
 #pragma unroll
   for (int j = 0; j < kSortItems; ++j) {
     const int64_t i = w0 + j * 32 + lane;
-    bool bad;
-    key[j] = i >= a.rows ? 0u : key_in ? key_in[i] : sort_key(a, i, bad);
-    pos[j] = i >= a.rows ? 0u : pos_in ? pos_in[i] : (uint32_t)i;
+    t.key[j] = i < a.rows ? sort_key(a, i, bad) : 0u;
+    t.pos[j] = (uint32_t)i;
   }
-  const int sh = pass * a.bits;
+  if (bad) set_status(a.ctrl, ST_BAD_INDEX);
+  for (int p = 0; p < a.passes; ++p) {
+    for (int i = threadIdx.x; i < kSortWarps * kMaxRadix / 8; i += kSortThreads)
+      reinterpret_cast<uint4*>(&s.cnt[0][0])[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    rank_tile(t, w0, a.rows, p * a.bits, radix, s.cnt[warp]);
+    __syncthreads();
+    uint32_t* total = s.total[p & 1];
+    sum_warps(s, radix, total);
+    cluster_meet();  // every tile's counts; and the scatter of the pass before is read
+    uint32_t all = 0, before = 0;
+    if ((int)threadIdx.x < radix) {
+      for (int r = 0; r < C; ++r) {
+        const uint32_t v = peer_u32(total + threadIdx.x, r);
+        all += v;
+        if (r < (int)blockIdx.x) before += v;
+      }
+    }
+    scan_digits(s, radix, all, before);
+    uint32_t* ko = p & 1 ? a.key[1] : a.key[0];
+    uint32_t* po = p & 1 ? a.pos[1] : a.pos[0];
+#pragma unroll
+    for (int j = 0; j < kSortItems; ++j) {
+      if (w0 + j * 32 + lane >= a.rows) continue;
+      const uint32_t d = (t.key[j] >> (p * a.bits)) & (radix - 1);
+      const uint32_t to = s.base[d] + s.cnt[warp][d] + t.rank[j];
+      ko[to] = t.key[j];
+      po[to] = t.pos[j];
+    }
+    if (p + 1 == a.passes) break;
+    cluster_meet();
+#pragma unroll
+    for (int j = 0; j < kSortItems; ++j) {
+      const int64_t i = w0 + j * 32 + lane;
+      if (i < a.rows) {
+        t.key[j] = __ldcg(ko + i);
+        t.pos[j] = __ldcg(po + i);
+      }
+    }
+  }
+  cluster_meet();  // no CTA leaves while another may read its counts
+}
+
+// Counts the first digit of every tile; the other blocks clear.
+__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortArgs a, ClearArgs c) {
+  __shared__ uint32_t cnt[kMaxRadix];
+  wait_prior_grid();
+  allow_next_grid();
+  if (blockIdx.x >= a.tiles) {
+    clear_rows(c, blockIdx.x - a.tiles, gridDim.x - a.tiles);
+    return;
+  }
+  const int radix = 1 << a.bits;
+  // the later passes' counts are added to: zero
+  const int64_t gn = a.tiles * kSortThreads;
+  for (int64_t i = (int64_t)blockIdx.x * kSortThreads + threadIdx.x;
+       i < (int64_t)(a.passes - 1) * a.tiles * radix; i += gn)
+    a.count[a.tiles * radix + i] = 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.owner[0] = 0;
+  for (int d = threadIdx.x; d < radix; d += kSortThreads) cnt[d] = 0;
+  __syncthreads();
+  bool bad = false;
 #pragma unroll
   for (int j = 0; j < kSortItems; ++j) {
-    const bool in = w0 + j * 32 + lane < a.rows;
-    const uint32_t d = in ? (key[j] >> sh) & (radix - 1) : 0xffffffffu;
-    const uint32_t same = __match_any_sync(0xffffffffu, d);
-    const int first = __ffs(same) - 1;
-    uint32_t old = 0;
-    if (in && lane == first) {
-      old = cnt[warp][d];
-      cnt[warp][d] = old + __popc(same);
+    const int64_t i = (int64_t)blockIdx.x * kTile + j * kSortThreads + threadIdx.x;
+    if (i < a.rows) atomicAdd(&cnt[sort_key(a, i, bad) & (radix - 1)], 1u);
+  }
+  if (bad) set_status(a.ctrl, ST_BAD_INDEX);
+  __syncthreads();
+  for (int d = threadIdx.x; d < radix; d += kSortThreads)
+    a.count[(int64_t)blockIdx.x * radix + d] = cnt[d];
+}
+
+__global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(SortArgs a, int pass) {
+  extern __shared__ __align__(16) uint8_t sort_smem[];
+  SortShared& s = *reinterpret_cast<SortShared*>(sort_smem);
+  wait_prior_grid();
+  allow_next_grid();
+  const int radix = 1 << a.bits, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t tile = blockIdx.x, w0 = tile * kTile + (int64_t)warp * kSortItems * 32;
+  const bool odd = pass & 1;
+  const uint32_t *ki = odd ? a.key[0] : a.key[1], *pi = odd ? a.pos[0] : a.pos[1];
+  uint32_t *ko = odd ? a.key[1] : a.key[0], *po = odd ? a.pos[1] : a.pos[0];
+  TileRanks t;
+#pragma unroll
+  for (int j = 0; j < kSortItems; ++j) {
+    const int64_t i = w0 + j * 32 + lane;
+    bool bad = false;
+    t.key[j] = i >= a.rows ? 0u : pass ? ki[i] : sort_key(a, i, bad);
+    t.pos[j] = i >= a.rows || !pass ? (uint32_t)i : pi[i];
+  }
+  for (int i = threadIdx.x; i < kSortWarps * kMaxRadix / 8; i += kSortThreads)
+    reinterpret_cast<uint4*>(&s.cnt[0][0])[i] = make_uint4(0, 0, 0, 0);
+  // this digit's counts, of earlier tiles and of all
+  const uint32_t* cp = a.count + (int64_t)pass * a.tiles * radix;
+  uint32_t before = 0, all = 0;
+  if ((int)threadIdx.x < radix) {
+#pragma unroll 8
+    for (int64_t r = 0; r < a.tiles; ++r) {
+      const uint32_t v = cp[r * radix + threadIdx.x];
+      all += v;
+      if (r < tile) before += v;
     }
-    old = __shfl_sync(0xffffffffu, old, first);
-    rank[j] = old + __popc(same & ((1u << lane) - 1u));
-    __syncwarp();
   }
   __syncthreads();
-  for (int d = threadIdx.x; d < radix; d += kSortThreads) {
-    uint32_t sum = base[d];
-    for (int w = 0; w < kWarps; ++w) {
-      const uint32_t v = cnt[w][d];
-      cnt[w][d] = sum;
-      sum += v;
-    }
-  }
+  rank_tile(t, w0, a.rows, pass * a.bits, radix, s.cnt[warp]);
   __syncthreads();
+  sum_warps(s, radix, s.total[0]);
+  scan_digits(s, radix, all, before);
   uint32_t* next = pass + 1 < a.passes ? a.count + (int64_t)(pass + 1) * a.tiles * radix : nullptr;
 #pragma unroll
   for (int j = 0; j < kSortItems; ++j) {
-    if (w0 + j * 32 + lane >= a.rows) break;
-    const uint32_t to = cnt[warp][(key[j] >> sh) & (radix - 1)] + rank[j];
-    key_out[to] = key[j];
-    pos_out[to] = pos[j];
+    if (w0 + j * 32 + lane >= a.rows) continue;
+    const uint32_t d = (t.key[j] >> (pass * a.bits)) & (radix - 1);
+    const uint32_t to = s.base[d] + s.cnt[warp][d] + t.rank[j];
+    ko[to] = t.key[j];
+    po[to] = t.pos[j];
     if (next)
-      atomicAdd(&next[(int64_t)(to / kTile) * radix + ((key[j] >> (sh + a.bits)) & (radix - 1))],
+      atomicAdd(&next[(int64_t)(to / kTile) * radix +
+                      ((t.key[j] >> ((pass + 1) * a.bits)) & (radix - 1))],
                 1u);
-    if (pass == 0 && key[j] < (uint32_t)a.vocab)
-      atomicOr(&a.seen[key[j] >> 5], 1u << (key[j] & 31));
   }
 }
 
 // ------------------------------------------------------------------ sums of the runs
 struct GradArgs {
-  const uint32_t *key, *pos, *seen;
+  const uint32_t *key, *pos;
   uint32_t* owner;
   float* part;
   int64_t rows, vocab, dim, ldd, ldg, chunk, chunks;
   float scale;
   int accumulate;
-  unsigned sum_blocks;  // blocks that sum; the others clear rows no token names
 };
 
 // kV columns of one table row: grad = scale * sum, or grad += scale * sum.
 template <class TG, int kV>
-__device__ __forceinline__ void put_row(TG* g, const float (&s)[kV], float scale, bool acc) {
+__device__ __forceinline__ void put_row(TG* g, const float* s, float scale, bool acc) {
   Pack<TG, kV>* p = reinterpret_cast<Pack<TG, kV>*>(g);
   Pack<TG, kV> o;
   if (acc) o = *p;
@@ -311,123 +444,144 @@ __device__ __forceinline__ void put_row(TG* g, const float (&s)[kV], float scale
   *p = o;
 }
 
-// blockDim (tx, ty): tx threads of kV columns each, ty chunks.  Items (chunk group, column
-// slab) with the slabs of a chunk group side by side.
-template <class TD, class TG, int kV>
+// blockDim (tx, ty): ty chunks; tx threads share a chunk's columns, each with kJ groups of
+// kV consecutive columns, the groups tx * kV apart (kV = 1, kJ = 8 where rows do not start
+// on 16-byte boundaries: as many loads in flight per token as one wide load brings).
+template <class TD, class TG, int kV, int kJ>
 __global__ void __launch_bounds__(128) grad_sum_kernel(GradArgs a, const TD* dout, TG* grad) {
   wait_prior_grid();
   allow_next_grid();
-  if (blockIdx.x >= a.sum_blocks) {  // rows that no token names: zeros
-    const int64_t nb = gridDim.x - a.sum_blocks;
-    const int tid = threadIdx.y * blockDim.x + threadIdx.x;
-    const int64_t warp = ((int64_t)(blockIdx.x - a.sum_blocks) * 128 + tid) >> 5;
-    const int lane = tid & 31;
-    for (int64_t v = warp; v < a.vocab; v += nb * 4) {
-      if (a.seen[v >> 5] >> (v & 31) & 1u) continue;
-      TG* g = grad + v * a.ldg;
-      for (int64_t col = (int64_t)lane * kV; col < a.dim; col += 32 * kV) {
-        Pack<TG, kV> z;
-#pragma unroll
-        for (int e = 0; e < kV; ++e) z.v[e] = Elem<TG>::put(0.0f);
-        *reinterpret_cast<Pack<TG, kV>*>(g + col) = z;
-      }
-    }
-    return;
-  }
-  const int64_t slabs = (a.dim + (int64_t)blockDim.x * kV - 1) / ((int64_t)blockDim.x * kV);
+  const int64_t span = (int64_t)blockDim.x * kV;
+  const int64_t slabs = (a.dim + span * kJ - 1) / (span * kJ);
   const int64_t slab = blockIdx.x % slabs;
   const int64_t c = blockIdx.x / slabs * blockDim.y + threadIdx.y;
-  const int64_t col = (slab * blockDim.x + threadIdx.x) * kV;
+  const int64_t col = slab * span * kJ + threadIdx.x * kV;
   if (c >= a.chunks || col >= a.dim) return;
+  const int groups = (int)((a.dim - col + span - 1) / span);  // of this thread, up to kJ
   const int64_t i0 = c * a.chunk, i1 = i0 + a.chunk < a.rows ? i0 + a.chunk : a.rows;
   const uint32_t before = i0 > 0 ? a.key[i0 - 1] : 0xffffffffu;
   const uint32_t after = i1 < a.rows ? a.key[i1] : 0xffffffffu;
-  float s[kV];
+  float s[kJ][kV];
 #pragma unroll
-  for (int e = 0; e < kV; ++e) s[e] = 0.0f;
+  for (int g = 0; g < kJ; ++g)
+#pragma unroll
+    for (int e = 0; e < kV; ++e) s[g][e] = 0.0f;
   int64_t start = i0;  // of the run being summed
-  constexpr int kU = 4;
+  constexpr int kU = kJ > 1 ? 2 : 4;
   for (int64_t i = i0; i < i1; i += kU) {
-    Pack<TD, kV> v[kU];
-    uint32_t k[kU + 1];
+    Pack<TD, kV> v[kU][kJ];
+    uint32_t k[kU];
 #pragma unroll
     for (int j = 0; j < kU; ++j) {
       k[j] = i + j < i1 ? a.key[i + j] : (uint32_t)a.vocab;
-      if (k[j] < (uint32_t)a.vocab)
-        v[j] = *reinterpret_cast<const Pack<TD, kV>*>(dout + (int64_t)a.pos[i + j] * a.ldd + col);
+      if (k[j] < (uint32_t)a.vocab) {
+        const TD* src = dout + (int64_t)a.pos[i + j] * a.ldd + col;
+#pragma unroll
+        for (int g = 0; g < kJ; ++g)
+          if (kJ == 1 || g < groups)
+            v[j][g] = *reinterpret_cast<const Pack<TD, kV>*>(src + g * span);
+      }
     }
-    k[kU] = i + kU < i1 ? a.key[i + kU] : after;
 #pragma unroll
     for (int j = 0; j < kU; ++j) {
       if (k[j] >= (uint32_t)a.vocab) break;  // dropped tokens sort last
 #pragma unroll
-      for (int e = 0; e < kV; ++e) s[e] += Elem<TD>::get(v[j].v[e]);
-      const uint32_t nk = i + j + 1 < i1 ? k[j + 1] : after;
+      for (int g = 0; g < kJ; ++g)
+#pragma unroll
+        for (int e = 0; e < kV; ++e)
+          if (kJ == 1 || g < groups) s[g][e] += Elem<TD>::get(v[j][g].v[e]);
       const bool last = i + j + 1 == i1;
+      const uint32_t nk = last ? after : j + 1 < kU ? k[j + 1 < kU ? j + 1 : 0] : a.key[i + kU];
       if (!last && nk == k[j]) continue;
       // the run ends here, or the chunk does
       const bool from = start == i0 && before == k[j];
       const bool on = last && after == k[j];
-      if (!from && !on) {
-        put_row<TG, kV>(grad + (int64_t)k[j] * a.ldg + col, s, a.scale, a.accumulate != 0);
-      } else {
-        Pack<float, kV> o;
 #pragma unroll
-        for (int e = 0; e < kV; ++e) o.v[e] = s[e];
-        *reinterpret_cast<Pack<float, kV>*>(a.part + (2 * c + (from ? 0 : 1)) * a.dim + col) = o;
-        if (!from && slab == 0 && threadIdx.x == 0)
-          a.owner[1 + atomicAdd(&a.owner[0], 1u)] = (uint32_t)c;
+      for (int g = 0; g < kJ; ++g) {
+        if (kJ > 1 && g >= groups) break;
+        if (!from && !on) {
+          put_row<TG, kV>(grad + (int64_t)k[j] * a.ldg + col + g * span, s[g], a.scale,
+                          a.accumulate != 0);
+        } else {
+          Pack<float, kV> o;
+#pragma unroll
+          for (int e = 0; e < kV; ++e) o.v[e] = s[g][e];
+          *reinterpret_cast<Pack<float, kV>*>(a.part + (2 * c + (from ? 0 : 1)) * a.dim + col +
+                                              g * span) = o;
+        }
+#pragma unroll
+        for (int e = 0; e < kV; ++e) s[g][e] = 0.0f;
       }
-#pragma unroll
-      for (int e = 0; e < kV; ++e) s[e] = 0.0f;
+      if (on && !from && slab == 0 && threadIdx.x == 0) {
+        // a run that goes on: chunks c+1 .. end-1 start with it
+        int64_t lo = c + 1, step = 1;
+        while (lo + step < a.chunks && a.key[(lo + step) * a.chunk] == k[j]) {
+          lo += step;
+          step *= 2;
+        }
+        int64_t hi = lo + step < a.chunks ? lo + step : a.chunks;
+        while (hi - lo > 1) {
+          const int64_t mid = (lo + hi) / 2;
+          if (a.key[mid * a.chunk] == k[j]) lo = mid; else hi = mid;
+        }
+        const uint32_t at = atomicAdd(&a.owner[0], 1u);
+        a.owner[2 + 2 * at] = (uint32_t)c;
+        a.owner[3 + 2 * at] = (uint32_t)(lo + 1);
+      }
       start = i + j + 1;
     }
   }
 }
 
 // Runs that cross chunk borders: the last partial of the chunk that the run starts in,
-// then the first partials of the chunks it goes on into, ascending.  A block joins 64
+// then the first partials of the chunks it goes on into, ascending.  A block joins 64 kV
 // columns of one run: four groups of threads each add every fourth chunk in order, and
 // the four sums are added in a fixed order.
-template <class TG>
+template <class TG, int kV>
 __global__ void __launch_bounds__(256) grad_join_kernel(GradArgs a, TG* grad) {
-  __shared__ float red[4][64];
+  __shared__ Pack<float, kV> red[4][64];
   wait_prior_grid();
   allow_next_grid();
   const int64_t n = a.owner[0];
-  const int64_t slabs = (a.dim + 63) / 64;
+  const int64_t slabs = (a.dim + 64 * kV - 1) / (64 * kV);
   const int x = threadIdx.x & 63, q = threadIdx.x >> 6;
   for (int64_t it = blockIdx.x; it < n * slabs; it += gridDim.x) {
-    const int64_t c = a.owner[1 + it / slabs];
-    const int64_t col = it % slabs * 64 + x;
-    const uint32_t k = a.key[(c + 1) * a.chunk];
-    // chunks c+1 .. e-1 start with this run
-    int64_t lo = c + 1, hi = a.chunks;
-    while (lo < hi) {
-      const int64_t mid = (lo + hi) / 2;
-      if (a.key[mid * a.chunk] == k) lo = mid + 1; else hi = mid;
-    }
-    float s = 0.0f;
+    const int64_t c = a.owner[2 + 2 * (it / slabs)], end = a.owner[3 + 2 * (it / slabs)];
+    const int64_t col = (it % slabs * 64 + x) * kV;
+    Pack<float, kV> s;
+#pragma unroll
+    for (int e = 0; e < kV; ++e) s.v[e] = 0.0f;
     if (col < a.dim) {
-      if (q == 0) s = a.part[(2 * c + 1) * a.dim + col];
+      // every fourth partial, the first of group 0 being the start chunk's last run
+      const float* p0 = a.part + (2 * c + 1) * a.dim + col;
+      const float* p = a.part + 2 * c * a.dim + col;
 #pragma unroll 4
-      for (int64_t j = c + 1 + q; j < lo; j += 4) s += a.part[2 * j * a.dim + col];
+      for (int64_t j = q; j < end - c; j += 4) {
+        const Pack<float, kV> v =
+            *reinterpret_cast<const Pack<float, kV>*>(j == 0 ? p0 : p + 2 * j * a.dim);
+#pragma unroll
+        for (int e = 0; e < kV; ++e) s.v[e] += v.v[e];
+      }
     }
     red[q][x] = s;
     __syncthreads();
     if (q == 0 && col < a.dim) {
-      const float t[1] = {(red[0][x] + red[1][x]) + (red[2][x] + red[3][x])};
-      put_row<TG, 1>(grad + (int64_t)k * a.ldg + col, t, a.scale, a.accumulate != 0);
+      float t[kV];
+#pragma unroll
+      for (int e = 0; e < kV; ++e)
+        t[e] = (red[0][x].v[e] + red[1][x].v[e]) + (red[2][x].v[e] + red[3][x].v[e]);
+      put_row<TG, kV>(grad + (int64_t)a.key[(c + 1) * a.chunk] * a.ldg + col, t, a.scale,
+                      a.accumulate != 0);
     }
     __syncthreads();
   }
 }
 
 template <class... P, class... A>
-cudaError_t launch(Ctx& c, unsigned grid, dim3 block, void (*fn)(P...), A... args) {
+cudaError_t launch(Ctx& c, int64_t grid, dim3 block, void (*fn)(P...), A... args) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = block;
   cfg.stream = c.stream;
   add_pdl_attr(c, cfg, attr);
@@ -436,27 +590,21 @@ cudaError_t launch(Ctx& c, unsigned grid, dim3 block, void (*fn)(P...), A... arg
 }
 
 template <class TD, class TG>
-cudaError_t sum_typed(const Mat& d, const Mat& g, GradArgs a, Ctx& c) {
+cudaError_t sum_typed(const Mat& d, const Mat& g, const GradArgs& a, Ctx& c) {
   constexpr int kV = 16 / sizeof(TD);
   const bool vec = rows_aligned(d, 16) && rows_aligned(g, kV * sizeof(TG));
-  const int v = vec ? kV : 1;
+  const int v = vec ? kV : 8;  // columns per thread
   const int64_t groups = (a.dim + v - 1) / v;
   unsigned tx = 8;
   while (tx < 128 && tx < groups) tx *= 2;
   const unsigned ty = 128 / tx;
   const int64_t slabs = (groups + tx - 1) / tx;
-  a.sum_blocks = (unsigned)((a.chunks + ty - 1) / ty * slabs);
-  // clearing blocks: enough warps to fill the GPU beside the summing ones
-  const int64_t want = (a.vocab + 3) / 4;
-  const unsigned clear =
-      a.accumulate ? 0u : (unsigned)(want < 8 * c.num_sms ? want : 8 * (int64_t)c.num_sms);
-  cudaError_t e = cudaSuccess;
-  if (a.sum_blocks + clear > 0)
-    e = launch(c, a.sum_blocks + clear, dim3(tx, ty),
-               vec ? grad_sum_kernel<TD, TG, kV> : grad_sum_kernel<TD, TG, 1>, a,
-               (const TD*)d.p, (TG*)g.p);
+  const cudaError_t e = launch(c, (a.chunks + ty - 1) / ty * slabs, dim3(tx, ty),
+                               vec ? grad_sum_kernel<TD, TG, kV, 1> : grad_sum_kernel<TD, TG, 1, 8>,
+                               a, (const TD*)d.p, (TG*)g.p);
   if (e != cudaSuccess || a.chunks < 2) return e;
-  return launch(c, 2 * c.num_sms, dim3(256), grad_join_kernel<TG>, a, (TG*)g.p);
+  return launch(c, 2 * c.num_sms, dim3(256),
+                vec ? grad_join_kernel<TG, 4> : grad_join_kernel<TG, 1>, a, (TG*)g.p);
 }
 
 template <class TD>
@@ -464,6 +612,47 @@ cudaError_t sum_from(const Mat& d, const Mat& g, const GradArgs& a, Ctx& c) {
   if (g.dtype == CASGD_F32) return sum_typed<TD, float>(d, g, a, c);
   if (g.dtype == CASGD_BF16) return sum_typed<TD, __nv_bfloat16>(d, g, a, c);
   return sum_typed<TD, __half>(d, g, a, c);
+}
+
+// The sort (and the clearing, unless the gradient is added to) into a.key / a.pos of the
+// last pass.
+cudaError_t launch_sort(const SortArgs& a, const ClearArgs& clear, Ctx& c) {
+  const size_t smem = sizeof(SortShared);
+  cudaError_t e = cudaFuncSetAttribute(
+      a.tiles <= kMaxCluster ? (const void*)sort_kernel : (const void*)sort_scatter_kernel,
+      cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  int64_t blocks = (clear.rows + kSortWarps - 1) / kSortWarps;  // a warp per row at most
+  if (blocks > 2 * c.num_sms) blocks = 2 * c.num_sms;
+  if (a.tiles > kMaxCluster) {
+    e = launch(c, a.tiles + blocks, dim3(kSortThreads), sort_count_kernel, a, clear);
+    for (int p = 0; p < a.passes && e == cudaSuccess; ++p) {
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr[1];
+      cfg.gridDim = dim3((unsigned)a.tiles);
+      cfg.blockDim = dim3(kSortThreads);
+      cfg.dynamicSmemBytes = smem;
+      cfg.stream = c.stream;
+      add_pdl_attr(c, cfg, attr);
+      ++c.launches;
+      e = cudaLaunchKernelEx(&cfg, sort_scatter_kernel, a, p);
+    }
+    return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)a.tiles;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)((1 + (blocks + a.tiles - 1) / a.tiles) * a.tiles));
+  cfg.blockDim = dim3(kSortThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = c.stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  add_pdl_attr(c, cfg, attr);
+  ++c.launches;
+  return cudaLaunchKernelEx(&cfg, sort_kernel, a, clear);
 }
 
 }  // namespace
@@ -486,21 +675,18 @@ cudaError_t launch_embed_grad(const Mat& d, Ids ids, float scale, int64_t pad, b
   const SortPlan sp = sort_plan(g.rows);
   char* base = static_cast<char*>(ws);
   auto at = [&](size_t o) { return reinterpret_cast<uint32_t*>(base + o); };
-  SortArgs s{ids, d.rows, g.rows, pad, L.tiles, sp.bits, sp.passes, at(L.off_count),
-             at(L.off_seen), at(L.off_owner), (int64_t)(L.seen_bytes / 4),
-             reinterpret_cast<Ctrl*>(ws)};
-  cudaError_t e = launch(c, (unsigned)L.tiles, dim3(kSortThreads), sort_count_kernel, s);
-  const uint32_t *kin = nullptr, *pin = nullptr;
-  for (int p = 0; p < sp.passes && d.rows > 0 && e == cudaSuccess; ++p) {
-    uint32_t *ko = at(L.off_key[p & 1]), *po = at(L.off_pos[p & 1]);
-    e = launch(c, (unsigned)L.tiles, dim3(kSortThreads), sort_scatter_kernel, s, p, kin, pin, ko,
-               po);
-    kin = ko;
-    pin = po;
-  }
-  if (e != cudaSuccess) return e;
-  GradArgs a{kin, pin, s.seen, s.owner, reinterpret_cast<float*>(base + L.off_part), d.rows,
-             g.rows, d.cols, d.ld, g.ld, L.chunk, L.chunks, scale, accumulate ? 1 : 0, 0};
+  const SortArgs s{ids, d.rows, g.rows, pad, L.tiles, sp.bits, sp.passes, at(L.off_count),
+                   {at(L.off_key[0]), at(L.off_key[1])}, {at(L.off_pos[0]), at(L.off_pos[1])},
+                   at(L.off_owner), reinterpret_cast<Ctrl*>(ws)};
+  const int64_t es = elem_bytes(g.dtype);
+  const ClearArgs clear{g.p, accumulate ? 0 : g.rows, g.cols * es, g.ld * es,
+                        rows_aligned(g, 16) ? 1 : 0};
+  const cudaError_t e = launch_sort(s, clear, c);
+  if (e != cudaSuccess || d.rows == 0) return e;
+  const int last = (sp.passes - 1) & 1;
+  const GradArgs a{s.key[last], s.pos[last], s.owner, reinterpret_cast<float*>(base + L.off_part),
+                   d.rows, g.rows, d.cols, d.ld, g.ld, L.chunk, L.chunks, scale,
+                   accumulate ? 1 : 0};
   if (d.dtype == CASGD_F32) return sum_from<float>(d, g, a, c);
   if (d.dtype == CASGD_BF16) return sum_from<__nv_bfloat16>(d, g, a, c);
   return sum_from<__half>(d, g, a, c);

@@ -141,7 +141,7 @@ def test_embed_grad_types(gpu_lib, ddt, gdt, accumulate):
 # rows: within one sorting tile, several tiles; vocabularies of one, two and three digits;
 # all tokens equal (one run through every chunk), all different, frequencies falling with
 # the rank, runs that end on chunk borders
-@pytest.mark.parametrize("rows", [0, 1, 2, 8, 9, 2047, 2049, 20000])
+@pytest.mark.parametrize("rows", [0, 1, 2, 8, 9, 2047, 2049, 8193, 20000, 65536, 65537, 150000])
 @pytest.mark.parametrize("vocab,kind", [(1, "same"), (7, "uniform"), (600, "same"),
                                         (600, "blocks"), (30000, "falling"),
                                         (300000, "uniform"), (300000, "last")])
