@@ -158,10 +158,9 @@ struct SortArgs {
   Ctrl* ctrl;
 };
 
-struct ClearArgs {  // the gradient as rows of 16-byte units, or of elements
+struct ClearArgs {  // rows of bytes
   void* p;
   int64_t rows, row_bytes, pitch_bytes;
-  int wide;
 };
 
 __device__ __forceinline__ uint32_t sort_key(const SortArgs& a, int64_t i, bool& bad) {
@@ -171,23 +170,20 @@ __device__ __forceinline__ uint32_t sort_key(const SortArgs& a, int64_t i, bool&
   return id == a.padding_id || out ? (uint32_t)a.vocab : (uint32_t)id;
 }
 
-// Zeros to the whole gradient: a warp per row.
+// Zeros to the rows: a warp per row, 16 bytes per lane between the row's first and last
+// 16-byte boundaries.
 __device__ void clear_rows(const ClearArgs& c, int64_t block, int64_t blocks) {
   const int64_t warp = block * kSortWarps + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   for (int64_t r = warp; r < c.rows; r += blocks * kSortWarps) {
     char* row = static_cast<char*>(c.p) + r * c.pitch_bytes;
-    if (c.wide) {
-      for (int64_t i = lane * 16; i < c.row_bytes; i += 512)
-        *reinterpret_cast<uint4*>(row + i) = make_uint4(0, 0, 0, 0);
-    } else if (c.row_bytes % 4 == 0 && c.pitch_bytes % 4 == 0 &&
-               reinterpret_cast<uintptr_t>(c.p) % 4 == 0) {
-      for (int64_t i = lane * 4; i < c.row_bytes; i += 128)
-        *reinterpret_cast<uint32_t*>(row + i) = 0u;
-    } else {
-      for (int64_t i = lane * 2; i < c.row_bytes; i += 64)
-        *reinterpret_cast<uint16_t*>(row + i) = 0;
-    }
+    int64_t head = (16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15;
+    if (head > c.row_bytes) head = c.row_bytes;
+    const int64_t tail = head + (c.row_bytes - head) / 16 * 16;
+    if (lane * 2 < head) *reinterpret_cast<uint16_t*>(row + lane * 2) = 0;
+    for (int64_t i = head + lane * 16; i < tail; i += 512)
+      *reinterpret_cast<uint4*>(row + i) = make_uint4(0, 0, 0, 0);
+    if (tail + lane * 2 < c.row_bytes) *reinterpret_cast<uint16_t*>(row + tail + lane * 2) = 0;
   }
 }
 
@@ -679,8 +675,7 @@ cudaError_t launch_embed_grad(const Mat& d, Ids ids, float scale, int64_t pad, b
                    {at(L.off_key[0]), at(L.off_key[1])}, {at(L.off_pos[0]), at(L.off_pos[1])},
                    at(L.off_owner), reinterpret_cast<Ctrl*>(ws)};
   const int64_t es = elem_bytes(g.dtype);
-  const ClearArgs clear{g.p, accumulate ? 0 : g.rows, g.cols * es, g.ld * es,
-                        rows_aligned(g, 16) ? 1 : 0};
+  const ClearArgs clear{g.p, accumulate ? 0 : g.rows, g.cols * es, g.ld * es};
   const cudaError_t e = launch_sort(s, clear, c);
   if (e != cudaSuccess || d.rows == 0) return e;
   const int last = (sp.passes - 1) & 1;

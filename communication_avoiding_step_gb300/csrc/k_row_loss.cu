@@ -33,155 +33,273 @@ __device__ __forceinline__ float fast_exp2(float t) {
   return r;
 }
 
-// The largest value m seen and the sum s of exp2((x - m) * scale) over the values seen
-// (m = -inf, s = 0: none).
+// Of the values x seen: the largest x * scale (m, rounded once) and the sum s of
+// 2^(x * scale - m), each exponent one fused multiply-add (m = -inf, s = 0: none seen).
+// scale is log2(e) over the temperature.
 struct MaxSum {
   float m, s;
 };
-__device__ __forceinline__ float rescale(float m, float top, float scale) {
-  return m == top ? 1.0f : fast_exp2((m - top) * scale);
+__device__ __forceinline__ float rescale(float m, float top) {
+  return m == top ? 1.0f : fast_exp2(m - top);
 }
-__device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b, float scale) {
+__device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b) {
   const float m = fmaxf(a.m, b.m);
-  return {m, a.s * rescale(a.m, m, scale) + b.s * rescale(b.m, m, scale)};
+  return {m, a.s * rescale(a.m, m) + b.s * rescale(b.m, m)};
 }
 template <int kLanes>
-__device__ __forceinline__ MaxSum join_lanes(MaxSum r, float scale) {
+__device__ __forceinline__ MaxSum join_lanes(MaxSum r) {
   float m = r.m;
 #pragma unroll
   for (int o = kLanes / 2; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float s = r.s * rescale(r.m, m, scale);
+  float s = r.s * rescale(r.m, m);
 #pragma unroll
   for (int o = kLanes / 2; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
   return {m, s};
 }
 
-// A row as granules of kV elements: element 0 is element `shift` of granule 0.
+// A granule: 16 bytes as four words, each kPer elements of the logits' type (kept as
+// words so that two 16-bit elements share a register).
+struct alignas(16) Granule {
+  uint32_t w[4];
+};
+template <class T>
+struct Words;
+template <>
+struct Words<float> {
+  static constexpr int kPer = 1;
+  static constexpr uint32_t kLowest = 0xff800000u;  // -inf
+  static __device__ __forceinline__ void get(uint32_t w, float (&f)[1]) {
+    f[0] = __uint_as_float(w);
+  }
+  static __device__ __forceinline__ uint32_t put(const float (&f)[1]) {
+    return __float_as_uint(f[0]);
+  }
+  static __device__ __forceinline__ uint32_t max(uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }
+};
+template <>
+struct Words<__nv_bfloat16> {
+  static constexpr int kPer = 2;
+  static constexpr uint32_t kLowest = 0xff80ff80u;
+  static __device__ __forceinline__ void get(uint32_t w, float (&f)[2]) {
+    f[0] = __uint_as_float(w << 16);
+    f[1] = __uint_as_float(w & 0xffff0000u);
+  }
+  static __device__ __forceinline__ uint32_t put(const float (&f)[2]) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(f[0], f[1]);
+    return reinterpret_cast<const uint32_t&>(v);
+  }
+  static __device__ __forceinline__ uint32_t max(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 v = __hmax2(reinterpret_cast<const __nv_bfloat162&>(a),
+                                     reinterpret_cast<const __nv_bfloat162&>(b));
+    return reinterpret_cast<const uint32_t&>(v);
+  }
+};
+template <>
+struct Words<__half> {
+  static constexpr int kPer = 2;
+  static constexpr uint32_t kLowest = 0xfc00fc00u;
+  static __device__ __forceinline__ void get(uint32_t w, float (&f)[2]) {
+    const float2 v = __half22float2(reinterpret_cast<const __half2&>(w));
+    f[0] = v.x;
+    f[1] = v.y;
+  }
+  static __device__ __forceinline__ uint32_t put(const float (&f)[2]) {
+    const __half2 v = __floats2half2_rn(f[0], f[1]);
+    return reinterpret_cast<const uint32_t&>(v);
+  }
+  static __device__ __forceinline__ uint32_t max(uint32_t a, uint32_t b) {
+    const __half2 v = __hmax2(reinterpret_cast<const __half2&>(a),
+                              reinterpret_cast<const __half2&>(b));
+    return reinterpret_cast<const uint32_t&>(v);
+  }
+};
+template <class T>
+__device__ __forceinline__ Granule no_granule() {
+  return {{Words<T>::kLowest, Words<T>::kLowest, Words<T>::kLowest, Words<T>::kLowest}};
+}
+// p with element e replaced by x's bits (e a constant after unrolling)
+template <class T>
+__device__ __forceinline__ void set_element(Granule& p, int e, T x) {
+  if (sizeof(T) == 4) {
+    p.w[e & 3] = reinterpret_cast<const uint32_t&>(x);
+  } else {
+    const uint32_t b = reinterpret_cast<const uint16_t&>(x);
+    p.w[(e >> 1) & 3] = e & 1 ? (p.w[(e >> 1) & 3] & 0xffffu) | (b << 16)
+                              : (p.w[(e >> 1) & 3] & 0xffff0000u) | b;
+  }
+}
+template <class T>
+__device__ __forceinline__ T element(const Granule& p, int e) {
+  if (sizeof(T) == 4) return reinterpret_cast<const T&>(p.w[e & 3]);
+  const uint16_t b = (uint16_t)(p.w[(e >> 1) & 3] >> (16 * (e & 1)));
+  return reinterpret_cast<const T&>(b);
+}
+template <class T>
+__device__ __forceinline__ T lowest() {
+  const uint32_t w = Words<T>::kLowest;
+  return reinterpret_cast<const T&>(w);
+}
+
+// Maximum and sum of kN granules (16-bit types compared two at a time).
+template <class T, int kN>
+__device__ __forceinline__ MaxSum granules_max_sum(const Granule (&p)[kN], float scale) {
+  using W = Words<T>;
+  uint32_t mw = p[0].w[0];
+#pragma unroll
+  for (int i = 1; i < 4 * kN; ++i) mw = W::max(mw, p[i / 4].w[i % 4]);
+  float mf[W::kPer];
+  W::get(mw, mf);
+  const float m = fmaxf(mf[0], mf[W::kPer - 1]) * scale;
+  const float base = m == -INFINITY ? 0.0f : m;
+  float s[4] = {};
+#pragma unroll
+  for (int i = 0; i < 4 * kN; ++i) {
+    float f[W::kPer];
+    W::get(p[i / 4].w[i % 4], f);
+#pragma unroll
+    for (int e = 0; e < W::kPer; ++e)
+      s[(i * W::kPer + e) & 3] += fast_exp2(fmaf(f[e], scale, -base));
+  }
+  return {m, (s[0] + s[1]) + (s[2] + s[3])};
+}
+
+// A row as granules of kV elements: element 0 is element `shift` of granule 0, and
+// granules whole0 .. whole1-1 hold elements of this row alone.
 template <class T>
 struct Row {
   static constexpr int kV = 16 / sizeof(T);
-  const T* x;   // element 0
-  int64_t n;
-  int shift;
-  int64_t granules;
+  const T* x;  // element 0
+  int n, shift, granules, whole0, whole1;
   __device__ __forceinline__ Row(const T* p, int64_t cols)
-      : x(p), n(cols), shift((int)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T))),
-        granules((cols + shift + kV - 1) / kV) {}
-  __device__ __forceinline__ int64_t first(int64_t g) const { return g * kV - shift; }
-  __device__ __forceinline__ bool whole(int64_t g) const {
-    return first(g) >= 0 && first(g) + kV <= n;
-  }
+      : x(p), n((int)cols), shift((int)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T))),
+        granules((int)((cols + shift + kV - 1) / kV)), whole0(shift ? 1 : 0),
+        whole1((int)((cols + shift) / kV)) {}
+  __device__ __forceinline__ int64_t first(int g) const { return (int64_t)g * kV - shift; }
+  __device__ __forceinline__ bool whole(int g) const { return g >= whole0 && g < whole1; }
   // granule g; -inf in the places of other rows' elements
-  __device__ __forceinline__ void load(int64_t g, float (&v)[kV]) const {
+  __device__ __forceinline__ Granule load(int g) const {
+    const T* p = x + first(g);
+    if (whole(g)) return *reinterpret_cast<const Granule*>(p);
+    Granule o = no_granule<T>();
     const int64_t i = first(g);
-    if (whole(g)) {
-      const Pack<T, kV> p = *reinterpret_cast<const Pack<T, kV>*>(x + i);
 #pragma unroll
-      for (int e = 0; e < kV; ++e) v[e] = Elem<T>::get(p.v[e]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < kV; ++e)
-        v[e] = i + e >= 0 && i + e < n ? Elem<T>::get(x[i + e]) : -INFINITY;
-    }
+    for (int e = 0; e < kV; ++e)
+      if (i + e >= 0 && i + e < n) set_element(o, e, p[e]);
+    return o;
   }
 };
 
-// Granule g of a gradient row (element 0 at `out`), laid over the granules of `r`.
-template <class T>
-__device__ __forceinline__ void put_granule(const Row<T>& r, T* out, bool aligned, int64_t g,
-                                            const float (&v)[Row<T>::kV]) {
-  constexpr int kV = Row<T>::kV;
-  Pack<T, kV> p;
-#pragma unroll
-  for (int e = 0; e < kV; ++e) p.v[e] = Elem<T>::put(v[e]);
-  const int64_t i = r.first(g);
-  if (aligned && r.whole(g)) {
-    *reinterpret_cast<Pack<T, kV>*>(out + i) = p;
-  } else {
-#pragma unroll
-    for (int e = 0; e < kV; ++e)
-      if (i + e >= 0 && i + e < r.n) out[i + e] = p.v[e];
-  }
-}
 template <class T>
 __device__ __forceinline__ bool same_phase(const T* a, const T* b) {
   return ((reinterpret_cast<uintptr_t>(a) ^ reinterpret_cast<uintptr_t>(b)) & 15) == 0;
 }
+// Granule g of a gradient row (element 0 at `out`), laid over the granules of `r`.
+template <class T>
+__device__ __forceinline__ void put_granule(const Row<T>& r, T* out, bool aligned, int g,
+                                            const Granule& p) {
+  constexpr int kV = Row<T>::kV;
+  T* dst = out + r.first(g);
+  if (aligned && r.whole(g)) {
+    *reinterpret_cast<Granule*>(dst) = p;
+  } else {
+    const int64_t i = r.first(g);
+#pragma unroll
+    for (int e = 0; e < kV; ++e)
+      if (i + e >= 0 && i + e < r.n) dst[e] = element<T>(p, e);
+  }
+}
 
-// Maximum and sum of a row by kT threads (a warp, or a block of kT); every thread gets them.
+// k * 2^(x * scale - m) of a granule: with k = -g / s, its gradient away from the target.
+template <class T>
+__device__ __forceinline__ Granule softmax_part(const Granule& x, float scale, float m, float k) {
+  using W = Words<T>;
+  Granule o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float f[W::kPer];
+    W::get(x.w[i], f);
+#pragma unroll
+    for (int e = 0; e < W::kPer; ++e) f[e] = k * fast_exp2(fmaf(f[e], scale, -m));
+    o.w[i] = W::put(f);
+  }
+  return o;
+}
+
+// Maximum and sum of a row by kT threads (a warp, or a block of kT); every thread gets
+// them.  Two groups of granules take turns: one is loaded while the other is summed.
 template <class T, int kT>
 __device__ MaxSum row_max_sum(const Row<T>& r, int tid, float scale) {
-  constexpr int kV = Row<T>::kV, kU = 4;
+  constexpr int kU = 4;
   MaxSum acc{-INFINITY, 0.0f};
-  for (int64_t g0 = tid; g0 < r.granules; g0 += kT * kU) {
-    float v[kU][kV];
+  Granule cur[kU], next[kU];
+  auto fetch = [&](Granule(&p)[kU], int g0) {
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      if (g0 + u * kT < r.granules) {
-        r.load(g0 + u * kT, v[u]);
-      } else {
+    for (int u = 0; u < kU; ++u)
+      p[u] = g0 + u * kT < r.granules ? r.load(g0 + u * kT) : no_granule<T>();
+  };
+  fetch(cur, tid);
+  for (int g0 = tid; g0 < r.granules; g0 += kT * kU) {
+    const bool more = g0 + kT * kU < r.granules;
+    if (more) fetch(next, g0 + kT * kU);
+    acc = join(acc, granules_max_sum<T, kU>(cur, scale));
+    if (more) {
 #pragma unroll
-        for (int e = 0; e < kV; ++e) v[u][e] = -INFINITY;
-      }
+      for (int u = 0; u < kU; ++u) cur[u] = next[u];
     }
-    float m = acc.m;
-#pragma unroll
-    for (int u = 0; u < kU; ++u)
-#pragma unroll
-      for (int e = 0; e < kV; ++e) m = fmaxf(m, v[u][e]);
-    const float base = m == -INFINITY ? 0.0f : m;
-    float s[kU] = {};
-#pragma unroll
-    for (int u = 0; u < kU; ++u)
-#pragma unroll
-      for (int e = 0; e < kV; ++e) s[u] += fast_exp2((v[u][e] - base) * scale);
-    acc.s = acc.s * rescale(acc.m, m, scale) + ((s[0] + s[1]) + (s[2] + s[3]));
-    acc.m = m;
   }
-  acc = join_lanes<32>(acc, scale);
+  acc = join_lanes<32>(acc);
   if (kT > 32) {
     __shared__ MaxSum part[kT / 32];
     __syncthreads();
     if ((tid & 31) == 0) part[tid >> 5] = acc;
     __syncthreads();
-    acc = join_lanes<kT / 32>(part[tid & (kT / 32 - 1)], scale);
+    acc = join_lanes<kT / 32>(part[tid & (kT / 32 - 1)]);
   }
   return acc;
 }
 
 // The target's log probability.
-__device__ __forceinline__ float log_prob(float xt, MaxSum r, float inv_t) {
-  return (xt - r.m) * inv_t - logf(r.s);
+__device__ __forceinline__ float log_prob(float xt, MaxSum r, float scale) {
+  constexpr float kLn2 = 0.6931471805599453f;
+  return fmaf(xt, scale, -r.m) * kLn2 - logf(r.s);
 }
 // g * (1 - softmax) at the target
 __device__ __forceinline__ float target_grad(float g, float xt, MaxSum r, float scale) {
-  return g * (1.0f - fast_exp2((xt - r.m) * scale) / r.s);
+  return g * (1.0f - fast_exp2(fmaf(xt, scale, -r.m)) / r.s);
 }
 
-// Writes g * (onehot - softmax), or zeros, for granules g0, g0 + step, .. of a row.
+// Writes g * (onehot - softmax), or zeros, for granules g0, g0 + step, .. below g1.
 template <class T>
-__device__ __forceinline__ void row_grad(const Row<T>& r, T* out, int64_t g0, int64_t g1,
-                                         int step, float scale, MaxSum ms, int64_t target,
+__device__ __forceinline__ void row_grad(const Row<T>& r, T* out, int g0, int g1, int step,
+                                         float scale, MaxSum ms, int64_t target,
                                          float g, bool zero) {
   constexpr int kV = Row<T>::kV, kU = 4;
   const bool al = same_phase(r.x, out);
   const float k = -g / ms.s;
-  for (int64_t i = g0; i < g1; i += (int64_t)step * kU) {
-    float v[kU][kV];
+  for (int i = g0; i < g1; i += step * kU) {
+    Granule v[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u)
-      if (!zero && i + (int64_t)u * step < g1) r.load(i + (int64_t)u * step, v[u]);
+      if (!zero && i + u * step < g1) v[u] = r.load(i + u * step);
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const int64_t gr = i + (int64_t)u * step;
+      const int gr = i + u * step;
       if (gr >= g1) break;
-      const int64_t t = target - r.first(gr);
+      Granule o{{0u, 0u, 0u, 0u}};
+      if (!zero) {
+        o = softmax_part<T>(v[u], scale, ms.m, k);
+        const int64_t t = target - r.first(gr);
+        if (t >= 0 && t < kV) {
 #pragma unroll
-      for (int e = 0; e < kV; ++e) {
-        const float p = fast_exp2((v[u][e] - ms.m) * scale);
-        v[u][e] = zero ? 0.0f : t == e ? g * (1.0f - p / ms.s) : k * p;
+          for (int e = 0; e < kV; ++e)
+            if (t == e)
+              set_element(o, e, Elem<T>::put(target_grad(
+                                    g, Elem<T>::get(element<T>(v[u], e)), ms, scale)));
+        }
       }
-      put_granule(r, out, al, gr, v[u]);
+      put_granule(r, out, al, gr, o);
     }
   }
 }
@@ -215,7 +333,7 @@ constexpr int64_t kWarpCols = 2048;
 
 // Each row's maximum, sum and log probability; kT threads per row.
 template <class T, int kT>
-__global__ void __launch_bounds__(kBlock) pref_stats_kernel(PrefArgs a, PrefWs w) {
+__global__ void __launch_bounds__(kBlock, 4) pref_stats_kernel(PrefArgs a, PrefWs w) {
   wait_prior_grid();
   allow_next_grid();
   const int tid = threadIdx.x % kT;
@@ -235,7 +353,7 @@ __global__ void __launch_bounds__(kBlock) pref_stats_kernel(PrefArgs a, PrefWs w
       w.m[t] = r.m;
       w.s[t] = r.s;
       w.coef[t] = 0.0f;
-      w.lp[t] = log_prob(Elem<T>::get(row.x[target]), r, 1.0f);
+      w.lp[t] = log_prob(Elem<T>::get(row.x[target]), r, kLog2e);
     }
   }
 }
@@ -333,7 +451,7 @@ __global__ void __launch_bounds__(kBlock) pref_pair_kernel(PrefArgs a, PrefWs w)
 // warps) are dealt to the blocks in descending order, so that the rows read last by
 // pref_stats_kernel, still in L2, come first.
 template <class T, int kT>
-__global__ void __launch_bounds__(kBlock) pref_grad_kernel(PrefArgs a, PrefWs w, int64_t segs) {
+__global__ void __launch_bounds__(kBlock, 5) pref_grad_kernel(PrefArgs a, PrefWs w, int64_t segs) {
   wait_prior_grid();
   allow_next_grid();
   const int tid = threadIdx.x % kT;
@@ -348,8 +466,8 @@ __global__ void __launch_bounds__(kBlock) pref_grad_kernel(PrefArgs a, PrefWs w,
     const MaxSum ms{w.m[t], w.s[t]};
     const bool zero = target < 0 || target >= a.logits.cols || g == 0.0f;
     const Row<T> row(static_cast<const T*>(a.logits.p) + t * a.logits.ld, a.logits.cols);
-    const int64_t g1 = segs == 1 || seg == segs - 1 ? row.granules : (seg + 1) * kSeg;
-    row_grad(row, static_cast<T*>(a.grad.p) + t * a.grad.ld, seg * kSeg + tid, g1, kT, kLog2e, ms,
+    const int g1 = seg == segs - 1 ? row.granules : (int)(seg + 1) * kSeg;
+    row_grad(row, static_cast<T*>(a.grad.p) + t * a.grad.ld, (int)seg * kSeg + tid, g1, kT, kLog2e, ms,
              target, g, zero);
   }
 }
@@ -381,12 +499,15 @@ __device__ __forceinline__ bool load_info(const PolicyArgs& a, int64_t t, RowInf
 // logits / temperature.
 struct RowLoss {
   float lp, loss, kl, clipped, g;
+  // No gradient: a masked row, one of weight zero, one held by the clip (but not one
+  // that is NaN).
+  __device__ __forceinline__ bool none() const { return g == 0.0f && lp == lp; }
 };
 __device__ __forceinline__ RowLoss policy_row(const PolicyArgs& a, const RowInfo& f, MaxSum r,
-                                              float inv_t) {
+                                              float inv_t, float scale) {
   RowLoss o{0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
   if (f.target < 0) return o;
-  o.lp = log_prob(f.xt, r, inv_t);
+  o.lp = log_prob(f.xt, r, scale);
   if (f.weight == 0.0f) return o;
   const float ratio = expf(o.lp - f.old_logp);
   const float held = fminf(fmaxf(ratio, 1.0f - a.clip_low), 1.0f + a.clip_high);
@@ -465,32 +586,35 @@ __global__ void __launch_bounds__(kBlock) policy_reread_kernel(PolicyArgs a, Pol
       f.xt = Elem<T>::get(row.x[f.target]);
       r = row_max_sum<T, kT>(row, tid, scale);
     }
-    const RowLoss o = policy_row(a, f, r, inv_t);
+    const RowLoss o = policy_row(a, f, r, inv_t, scale);
     if (tid == 0) put_row_loss(a, w, t, o);
     if (a.grad.p)
-      row_grad(row, static_cast<T*>(a.grad.p) + t * a.grad.ld, (int64_t)tid, row.granules, kT,
-               scale, r, f.target, o.g, f.target < 0 || f.weight == 0.0f);
+      row_grad(row, static_cast<T*>(a.grad.p) + t * a.grad.ld, tid, row.granules, kT,
+               scale, r, f.target, o.g, f.weight == 0.0f || o.none());
   }
   policy_sums(a, w, gridDim.x, 0);
 }
 
 // Rows held on chip.  A cluster of C CTAs takes a row, each CTA a slice of up to
 // kBlock * kQ granules, kQ per thread.  A producer warp copies the slices of the next rows
-// into a ring of three stages with bulk copies and passes the row's scalars along; the
-// other warps turn a stage into exponentials against the thread's own maximum, kept in
-// registers (so the stage is free again before the row's sum is known), exchange one
-// (maximum, sum) pair per warp with the whole cluster through distributed shared memory,
-// and scale their exponentials into the gradient.  One read and one write per element,
-// one exponential, and one exchange per row.
+// into a ring of three stages with bulk copies and passes the row's scalars along.  The
+// other warps work on two rows in turn: the maximum and sum of the next row's slice, sent
+// as one pair per warp to every CTA of the cluster (distributed shared memory), then, with
+// the pairs of the row before it long arrived, that row's gradient from its stage.  So one
+// read and one write per element, two exponentials, and an exchange per row that nothing
+// waits for.
 constexpr int kStages = 3;
 constexpr int kConsumers = kBlock, kRingThreads = kBlock + 32;
 constexpr int kWarps = kConsumers / 32;
 constexpr int kMaxCluster = 8;
+constexpr int kExchanges = 4;
 constexpr uint64_t kTimeoutNs = 1000000000ull;
 
 struct RingShared {
-  uint64_t full[kStages], empty[kStages], red[2];
-  uint64_t pair[2][kMaxCluster * kWarps];  // (max, sum) of every warp of the cluster
+  // Four exchanges: a peer sends row i + 4's pairs only after this CTA sent row i + 2's,
+  // which it does after it has read row i's.
+  uint64_t full[kStages], empty[kStages], red[kExchanges];
+  uint64_t pair[kExchanges][kMaxCluster * kWarps];  // (max, sum) of every warp of the cluster
   RowInfo info[kStages];
   volatile uint32_t abort;
 };
@@ -550,10 +674,10 @@ constexpr size_t ring_bytes() {
   return (size_t)kStages * kBlock * kQ * 16 + sizeof(RingShared) + 16;
 }
 
-// Blocks per SM: as many as the stages leave room for, and the registers that hold a row.
+// Blocks per SM: as many as the stages leave shared memory for, up to three.
 template <class T, int kQ>
 constexpr int ring_blocks() {
-  return kQ * 16 / sizeof(T) <= 16 ? 3 : sizeof(T) == 2 ? 2 : 1;
+  return kQ <= 4 ? 3 : kQ <= 8 ? 2 : 1;
 }
 
 template <class T, int kQ>
@@ -570,8 +694,7 @@ __global__ void __launch_bounds__(kRingThreads, ring_blocks<T, kQ>())
       mbar_init(&sh->full[i], 1);
       mbar_init(&sh->empty[i], kWarps);
     }
-    mbar_init(&sh->red[0], 1);
-    mbar_init(&sh->red[1], 1);
+    for (int i = 0; i < kExchanges; ++i) mbar_init(&sh->red[i], 1);
     sh->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -605,19 +728,19 @@ __global__ void __launch_bounds__(kRingThreads, ring_blocks<T, kQ>())
         const int64_t target = __shfl_sync(0xffffffffu, mine.target, i);
         if (lane == i) sh->info[stage] = mine;
         uint32_t bytes = 0;
-        int64_t b0 = 0, c0 = 0;
+        int b0 = 0, c0 = 0;
         const Row<T> row(logits + t * a.logits.ld, a.logits.cols);
         T* buf = reinterpret_cast<T*>(ring + (size_t)stage * kBlock * kQ * 16);
         if (target >= 0) {
-          const int64_t per = (row.granules + C - 1) / C;
-          c0 = rank * per;
-          const int64_t c1 = c0 + per < row.granules ? c0 + per : row.granules;
+          const int per = (row.granules + C - 1) / C;
+          c0 = (int)rank * per;
+          const int c1 = c0 + per < row.granules ? c0 + per : row.granules;
           if (c0 < c1) {
             // granules shared with other rows: their elements one by one (lanes 0-15)
             b0 = row.whole(c0) ? c0 : c0 + 1;
-            int64_t b1 = c1 > b0 && !row.whole(c1 - 1) ? c1 - 1 : c1;
+            int b1 = c1 > b0 && !row.whole(c1 - 1) ? c1 - 1 : c1;
             if (b1 < b0) b1 = b0;
-            const int64_t eg = lane < 8 ? c0 : c1 - 1;
+            const int eg = lane < 8 ? c0 : c1 - 1;
             const int e = lane & 7;
             if (lane < 16 && e < kV && (lane < 8 ? b0 > c0 : b1 < c1 && b1 >= b0)) {
               const int64_t el = row.first(eg) + e;
@@ -655,101 +778,96 @@ __global__ void __launch_bounds__(kRingThreads, ring_blocks<T, kQ>())
     __syncwarp();
   } else {
     // ---------------------------------------------------------------- the other warps
+    const Granule* bufs = reinterpret_cast<const Granule*>(ring);
+    // stage and phase of the next row to sum, exchange numbers of the next row to sum and
+    // of the next to write
     int stage = 0;
-    uint32_t phase = 0, count = 0;
-    for (int64_t t = cluster; t < a.logits.rows; t += clusters) {
-      if (!__all_sync(0xffffffffu, ring_wait<false>(&sh->full[stage], phase, sh, w.ctrl))) break;
-      const RowInfo f = sh->info[stage];
-      const Row<T> row(logits + t * a.logits.ld, a.logits.cols);
-      const int64_t per = (row.granules + C - 1) / C, c0 = rank * per;
-      const int n = (int)(c0 + per < row.granules ? per : c0 < row.granules ? row.granules - c0 : 0);
-      float e[kQ][kV];
-      MaxSum mine{-INFINITY, 0.0f}, r{0.0f, 1.0f};
-      if (f.target >= 0) {
-        const Pack<T, kV>* buf =
-            reinterpret_cast<const Pack<T, kV>*>(ring + (size_t)stage * kBlock * kQ * 16);
+    uint32_t phase = 0, sent = 0, taken = 0;
+    auto slice = [&](const Row<T>& row, int& c0) {
+      const int per = (row.granules + C - 1) / C;
+      c0 = (int)rank * per;
+      return c0 + per < row.granules ? per : c0 < row.granules ? row.granules - c0 : 0;
+    };
+    auto sum_row = [&](int64_t t) -> bool {  // the next stage's row: sum it, send the pairs
+      if (!__all_sync(0xffffffffu, ring_wait<false>(&sh->full[stage], phase, sh, w.ctrl)))
+        return false;
+      if (sh->info[stage].target >= 0) {
+        const Row<T> row(logits + t * a.logits.ld, a.logits.cols);
+        int c0;
+        const int n = slice(row, c0);
+        Granule p[kQ];
 #pragma unroll
         for (int q = 0; q < kQ; ++q) {
           const int i = threadIdx.x + q * kBlock;
-          if (i < n) {
-            const Pack<T, kV> p = buf[i];
+          p[q] = i < n ? bufs[stage * kBlock * kQ + i] : no_granule<T>();
+          if (i < n && !row.whole(c0 + i)) {
+            const int64_t el = row.first(c0 + i);
 #pragma unroll
-            for (int j = 0; j < kV; ++j) e[q][j] = Elem<T>::get(p.v[j]);
-            if (!row.whole(c0 + i)) {
-              const int64_t el = row.first(c0 + i);
-#pragma unroll
-              for (int j = 0; j < kV; ++j)
-                if (el + j < 0 || el + j >= row.n) e[q][j] = -INFINITY;
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < kV; ++j) e[q][j] = -INFINITY;
+            for (int j = 0; j < kV; ++j)
+              if (el + j < 0 || el + j >= row.n) set_element(p[q], j, lowest<T>());
           }
         }
+        const MaxSum wp = join_lanes<32>(granules_max_sum<T, kQ>(p, scale));
+        uint64_t* bar = &sh->red[sent % kExchanges];
+        if (threadIdx.x == 0) mbar_expect_tx(bar, (uint32_t)(C * kWarps * 8));
+        if (lane < C)
+          send_pair(sh->pair[sent % kExchanges] + rank * kWarps + warp, bar, lane,
+                    (uint64_t)__float_as_uint(wp.s) << 32 | __float_as_uint(wp.m));
+        ++sent;
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->empty[stage]);
       if (++stage == kStages) {
         stage = 0;
         phase ^= 1u;
       }
+      return true;
+    };
+    bool ok = cluster < a.logits.rows && sum_row(cluster);
+    int ws = 0;  // stage of the row to write
+    for (int64_t t = cluster; t < a.logits.rows && ok; t += clusters) {
+      if (t + clusters < a.logits.rows) ok = sum_row(t + clusters);
+      if (!ok) break;
+      const RowInfo f = sh->info[ws];
+      MaxSum r{0.0f, 1.0f};
       if (f.target >= 0) {
-        float top = -INFINITY;
-#pragma unroll
-        for (int q = 0; q < kQ; ++q)
-#pragma unroll
-          for (int j = 0; j < kV; ++j) top = fmaxf(top, e[q][j]);
-        const float base = top == -INFINITY ? 0.0f : top;
-        float s[4] = {};
-#pragma unroll
-        for (int q = 0; q < kQ; ++q)
-#pragma unroll
-          for (int j = 0; j < kV; ++j) {
-            e[q][j] = fast_exp2((e[q][j] - base) * scale);
-            s[j & 3] += e[q][j];
-          }
-        mine = {top, (s[0] + s[1]) + (s[2] + s[3])};
-        const MaxSum wp = join_lanes<32>(mine, scale);
-        uint64_t* slots = sh->pair[count & 1];
-        uint64_t* bar = &sh->red[count & 1];
-        if (threadIdx.x == 0) mbar_expect_tx(bar, (uint32_t)(C * kWarps * 8));
-        if (lane < C)
-          send_pair(slots + rank * kWarps + warp, bar, lane,
-                    (uint64_t)__float_as_uint(wp.s) << 32 | __float_as_uint(wp.m));
-        if (!__all_sync(0xffffffffu, ring_wait<true>(bar, (count >> 1) & 1u, sh, w.ctrl))) break;
-        ++count;
+        const int e = taken % kExchanges;
+        ok = __all_sync(0xffffffffu, ring_wait<true>(&sh->red[e], (taken / kExchanges) & 1u, sh,
+                                                     w.ctrl));
+        if (!ok) break;
+        ++taken;
         MaxSum x{-INFINITY, 0.0f}, y{-INFINITY, 0.0f};
         if (lane < C * kWarps) {
-          const uint64_t v = slots[lane];
+          const uint64_t v = sh->pair[e][lane];
           x = {__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32))};
         }
         if (lane + 32 < C * kWarps) {
-          const uint64_t v = slots[lane + 32];
+          const uint64_t v = sh->pair[e][lane + 32];
           y = {__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32))};
         }
-        r = join_lanes<32>(join(x, y, scale), scale);
+        r = join_lanes<32>(join(x, y));
       }
-      const RowLoss o = policy_row(a, f, r, inv_t);
+      const RowLoss o = policy_row(a, f, r, inv_t, scale);
       if (rank == 0 && threadIdx.x == 0) put_row_loss(a, w, t, o);
-      if (!a.grad.p) continue;
-      T* out = static_cast<T*>(a.grad.p) + t * a.grad.ld;
-      const bool al = same_phase(row.x, out);
-      const bool zero = f.target < 0 || f.weight == 0.0f;
-      const float k = zero ? 0.0f : -o.g / r.s * rescale(mine.m, r.m, scale);
-#pragma unroll
-      for (int q = 0; q < kQ; ++q) {
-        const int i = threadIdx.x + q * kBlock;
-        if (i >= n) break;
-        float v[kV];
-#pragma unroll
-        for (int j = 0; j < kV; ++j) v[j] = zero ? 0.0f : k * e[q][j];
-        put_granule(row, out, al, c0 + i, v);
+      if (a.grad.p) {
+        const Row<T> row(logits + t * a.logits.ld, a.logits.cols);
+        int c0;
+        const int n = slice(row, c0);
+        T* out = static_cast<T*>(a.grad.p) + t * a.grad.ld;
+        const bool al = same_phase(row.x, out), zero = f.weight == 0.0f || o.none();
+        const float k = -o.g / r.s;
+        const Granule* buf = bufs + ws * kBlock * kQ;
+        // the granule that holds the target is set by the thread that stores it
+        const int tg = zero ? -1 : (int)((f.target + row.shift) / kV) - c0;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < n; i += kBlock) {
+          const Granule v = zero ? Granule{{0u, 0u, 0u, 0u}}
+                                 : softmax_part<T>(buf[i], scale, r.m, k);
+          put_granule(row, out, al, c0 + i, v);
+          if (i == tg) out[f.target] = Elem<T>::put(target_grad(o.g, f.xt, r, scale));
+        }
       }
-      if (!zero) {  // the thread that stored the target's granule sets the target
-        const int64_t i = (f.target + row.shift) / kV - c0;
-        if (i >= 0 && i < n && (int)(i % kBlock) == (int)threadIdx.x)
-          out[f.target] = Elem<T>::put(target_grad(o.g, f.xt, r, scale));
-      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->empty[ws]);
+      ws = ws + 1 == kStages ? 0 : ws + 1;
     }
     if (rank == 0) policy_sums(a, w, (unsigned)clusters, 1);
   }

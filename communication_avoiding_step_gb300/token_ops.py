@@ -23,10 +23,12 @@ from ._native import (
 _DTYPES = {torch.float32: CASGD_F32, torch.bfloat16: CASGD_BF16, torch.float16: CASGD_F16}
 
 
-def _stream(stream) -> C.c_void_p:
+# (Pointers go to ctypes as plain integers, and each tensor is looked at once: the smallest
+# calls take as long as their Python does.)
+def _stream(stream) -> int:
     if stream is None:
         stream = torch.cuda.current_stream()
-    return C.c_void_p(stream.cuda_stream)
+    return stream.cuda_stream
 
 
 def _matrix(t: torch.Tensor, name: str) -> Matrix:
@@ -37,13 +39,16 @@ def _matrix(t: torch.Tensor, name: str) -> Matrix:
     if dtype is None:
         raise ValueError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
     rows, cols = t.shape
-    ld, inner = t.stride()
     if cols < 1:
         raise ValueError(f"{name} must have at least one column")
-    if rows <= 1:
-        ld = max(ld, cols)
-    if (inner != 1 and cols > 1) or ld < cols:
-        raise ValueError(f"{name} must have contiguous, non-overlapping rows")
+    if t.is_contiguous():
+        ld = cols
+    else:
+        ld, inner = t.stride()
+        if rows <= 1:
+            ld = max(ld, cols)
+        if (inner != 1 and cols > 1) or ld < cols:
+            raise ValueError(f"{name} must have contiguous, non-overlapping rows")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     return Matrix(t.data_ptr(), rows, cols, ld, dtype)
@@ -59,21 +64,21 @@ def _tokens(t: torch.Tensor, name: str) -> Tokens:
     return Tokens(t.data_ptr(), t.numel(), 1 if t.dtype == torch.int64 else 0)
 
 
-def _vector(t: torch.Tensor, name: str, dtype, numel: int) -> C.c_void_p:
+def _vector(t: torch.Tensor, name: str, dtype, numel: int) -> int:
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.numel() < numel:
         raise ValueError(f"{name} must be a {dtype} tensor of at least {numel} elements")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return C.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _workspace(size_call: str, *args, device="cuda", stream=None) -> torch.Tensor:
     nbytes = C.c_size_t(0)
     _check(getattr(load(), size_call)(*args, C.byref(nbytes)), size_call)
     ws = torch.empty(nbytes.value, dtype=torch.uint8, device=device)
-    _check(load().casgd_workspace_init(C.c_void_p(ws.data_ptr()), ws.numel(), _stream(stream)),
+    _check(load().casgd_workspace_init(ws.data_ptr(), ws.numel(), _stream(stream)),
            "casgd_workspace_init")
     return ws
 
@@ -82,7 +87,7 @@ def _ws(ws: torch.Tensor) -> tuple:
     if not isinstance(ws, torch.Tensor) or not ws.is_cuda or ws.dtype != torch.uint8 \
             or not ws.is_contiguous():
         raise ValueError("ws must be a contiguous uint8 CUDA tensor (see the *_workspace calls)")
-    return C.c_void_p(ws.data_ptr()), ws.numel()
+    return ws.data_ptr(), ws.numel()
 
 
 # ---------------------------------------------------------------------------- embedding
