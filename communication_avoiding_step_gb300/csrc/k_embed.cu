@@ -19,37 +19,47 @@ constexpr size_t kAlign = 256;
 inline size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
 // ------------------------------------------------------------------ lookup
-// One thread per kV consecutive columns (kV = 1 where rows are not 16-byte aligned) and
-// kRows rows, so that several independent loads are in flight.
-constexpr int kRows = 4;
+// blockDim (tx, ty): tx threads share a row, each with kJ groups of kV consecutive columns,
+// the groups tx * kV apart (kV = 1 where rows do not start on 16-byte boundaries), and take
+// kRows rows at once: kJ * kRows independent loads in flight per thread.
+constexpr int kRows = 2, kCols = 4;
 
 template <class TI, class TO, int kV>
 __global__ void __launch_bounds__(256)
-    embed_kernel(const TI* table, int64_t vocab, int64_t dim, int64_t ldt, Ids ids, int64_t rows,
+    embed_kernel(const TI* table, int64_t vocab, int dim, int64_t ldt, Ids ids, int64_t rows,
                  float scale, int64_t padding_id, TO* out, int64_t ldo, Ctrl* ctrl) {
   wait_prior_grid();
   allow_next_grid();
-  const int64_t col = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * kV;
+  const int span = blockDim.x * kV;
+  const int c0 = blockIdx.x * span * kCols + threadIdx.x * kV;
   for (int64_t r0 = ((int64_t)blockIdx.y * blockDim.y + threadIdx.y) * kRows; r0 < rows;
        r0 += (int64_t)gridDim.y * blockDim.y * kRows) {
-    if (col >= dim) continue;
-    Pack<TI, kV> v[kRows];
+    Pack<TI, kV> v[kRows][kCols];
     bool have[kRows];
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
       const int64_t id = r0 + j < rows ? ids.at(r0 + j) : padding_id;
       have[j] = id != padding_id && id >= 0 && id < vocab;
-      if (r0 + j < rows && id != padding_id && !have[j] && col == 0) set_status(ctrl, ST_BAD_INDEX);
-      if (have[j]) v[j] = *reinterpret_cast<const Pack<TI, kV>*>(table + id * ldt + col);
+      if (r0 + j < rows && id != padding_id && !have[j] && c0 == 0) set_status(ctrl, ST_BAD_INDEX);
+      const TI* src = table + id * ldt + c0;
+#pragma unroll
+      for (int g = 0; g < kCols; ++g)
+        if (have[j] && c0 + g * span < dim)
+          v[j][g] = *reinterpret_cast<const Pack<TI, kV>*>(src + g * span);
     }
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
       if (r0 + j >= rows) break;
-      Pack<TO, kV> o;
+      TO* dst = out + (r0 + j) * ldo + c0;
 #pragma unroll
-      for (int e = 0; e < kV; ++e)
-        o.v[e] = Elem<TO>::put(have[j] ? scale * Elem<TI>::get(v[j].v[e]) : 0.0f);
-      *reinterpret_cast<Pack<TO, kV>*>(out + (r0 + j) * ldo + col) = o;
+      for (int g = 0; g < kCols; ++g) {
+        if (c0 + g * span >= dim) break;
+        Pack<TO, kV> o;
+#pragma unroll
+        for (int e = 0; e < kV; ++e)
+          o.v[e] = Elem<TO>::put(have[j] ? scale * Elem<TI>::get(v[j][g].v[e]) : 0.0f);
+        *reinterpret_cast<Pack<TO, kV>*>(dst + g * span) = o;
+      }
     }
   }
 }
@@ -61,20 +71,23 @@ cudaError_t embed_typed(const Mat& t, Ids ids, float scale, int64_t pad, const M
   const bool vec = t.cols % kV == 0 && rows_aligned(t, kV * sizeof(TI)) &&
                    rows_aligned(o, kV * sizeof(TO));
   const int64_t groups = vec ? t.cols / kV : t.cols;
+  // Threads per row: enough for kCols groups each, more where there are few rows to fill
+  // the GPU with.
+  const int64_t share = o.rows < 8 * c.num_sms ? 1 : kCols;
   unsigned tx = 32;
-  while (tx < 256 && tx < groups) tx *= 2;
+  while (tx < 256 && tx * share < groups) tx *= 2;
   const unsigned ty = 256 / tx;
+  const int64_t gx = (groups + tx * kCols - 1) / (tx * kCols);
   const int64_t gy = (o.rows + ty * kRows - 1) / (ty * kRows);
-  const dim3 grid((unsigned)((groups + tx - 1) / tx), (unsigned)(gy < 65535 ? gy : 65535));
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  cfg.gridDim = grid;
+  cfg.gridDim = dim3((unsigned)gx, (unsigned)(gy < 65535 ? gy : 65535));
   cfg.blockDim = dim3(tx, ty);
   cfg.stream = c.stream;
   add_pdl_attr(c, cfg, attr);
   ++c.launches;
   return cudaLaunchKernelEx(&cfg, vec ? embed_kernel<TI, TO, kV> : embed_kernel<TI, TO, 1>,
-                            (const TI*)t.p, t.rows, t.cols, t.ld, ids, o.rows, scale, pad,
+                            (const TI*)t.p, t.rows, (int)t.cols, t.ld, ids, o.rows, scale, pad,
                             (TO*)o.p, o.ld, ctrl);
 }
 
@@ -530,44 +543,57 @@ __global__ void __launch_bounds__(128) grad_sum_kernel(GradArgs a, const TD* dou
 }
 
 // Runs that cross chunk borders: the last partial of the chunk that the run starts in,
-// then the first partials of the chunks it goes on into, ascending.  A block joins 64 kV
-// columns of one run: four groups of threads each add every fourth chunk in order, and
-// the four sums are added in a fixed order.
-template <class TG, int kV>
+// then the first partials of the chunks it goes on into, ascending.  A block joins 256
+// columns of one run: four groups of 64 threads each add every fourth chunk in order, and
+// the four sums are added in a fixed order.  A thread's four columns are consecutive, or
+// 64 apart where rows do not start on 16-byte boundaries.
+template <class TG, bool kVec>
 __global__ void __launch_bounds__(256) grad_join_kernel(GradArgs a, TG* grad) {
-  __shared__ Pack<float, kV> red[4][64];
+  __shared__ float4 red[4][64];
   wait_prior_grid();
   allow_next_grid();
   const int64_t n = a.owner[0];
-  const int64_t slabs = (a.dim + 64 * kV - 1) / (64 * kV);
+  const int64_t slabs = (a.dim + 255) / 256;
   const int x = threadIdx.x & 63, q = threadIdx.x >> 6;
   for (int64_t it = blockIdx.x; it < n * slabs; it += gridDim.x) {
     const int64_t c = a.owner[2 + 2 * (it / slabs)], end = a.owner[3 + 2 * (it / slabs)];
-    const int64_t col = (it % slabs * 64 + x) * kV;
-    Pack<float, kV> s;
-#pragma unroll
-    for (int e = 0; e < kV; ++e) s.v[e] = 0.0f;
-    if (col < a.dim) {
+    const int64_t col = it % slabs * 256 + (kVec ? 4 * x : x);
+    const int64_t left = a.dim - col;
+    float s[4] = {};
+    if (left > 0) {
       // every fourth partial, the first of group 0 being the start chunk's last run
       const float* p0 = a.part + (2 * c + 1) * a.dim + col;
       const float* p = a.part + 2 * c * a.dim + col;
 #pragma unroll 4
       for (int64_t j = q; j < end - c; j += 4) {
-        const Pack<float, kV> v =
-            *reinterpret_cast<const Pack<float, kV>*>(j == 0 ? p0 : p + 2 * j * a.dim);
+        const float* src = j == 0 ? p0 : p + 2 * j * a.dim;
+        if (kVec) {
+          const float4 v = *reinterpret_cast<const float4*>(src);
+          s[0] += v.x;
+          s[1] += v.y;
+          s[2] += v.z;
+          s[3] += v.w;
+        } else {
 #pragma unroll
-        for (int e = 0; e < kV; ++e) s.v[e] += v.v[e];
+          for (int e = 0; e < 4; ++e)
+            if (64 * e < left) s[e] += src[64 * e];
+        }
       }
     }
-    red[q][x] = s;
+    red[q][x] = make_float4(s[0], s[1], s[2], s[3]);
     __syncthreads();
-    if (q == 0 && col < a.dim) {
-      float t[kV];
+    if (q == 0 && left > 0) {
+      const float4 r0 = red[0][x], r1 = red[1][x], r2 = red[2][x], r3 = red[3][x];
+      const float t[4] = {(r0.x + r1.x) + (r2.x + r3.x), (r0.y + r1.y) + (r2.y + r3.y),
+                          (r0.z + r1.z) + (r2.z + r3.z), (r0.w + r1.w) + (r2.w + r3.w)};
+      TG* dst = grad + (int64_t)a.key[(c + 1) * a.chunk] * a.ldg + col;
+      if (kVec) {
+        put_row<TG, 4>(dst, t, a.scale, a.accumulate != 0);
+      } else {
 #pragma unroll
-      for (int e = 0; e < kV; ++e)
-        t[e] = (red[0][x].v[e] + red[1][x].v[e]) + (red[2][x].v[e] + red[3][x].v[e]);
-      put_row<TG, kV>(grad + (int64_t)a.key[(c + 1) * a.chunk] * a.ldg + col, t, a.scale,
-                      a.accumulate != 0);
+        for (int e = 0; e < 4; ++e)
+          if (64 * e < left) put_row<TG, 1>(dst + 64 * e, t + e, a.scale, a.accumulate != 0);
+      }
     }
     __syncthreads();
   }
@@ -599,8 +625,10 @@ cudaError_t sum_typed(const Mat& d, const Mat& g, const GradArgs& a, Ctx& c) {
                                vec ? grad_sum_kernel<TD, TG, kV, 1> : grad_sum_kernel<TD, TG, 1, 8>,
                                a, (const TD*)d.p, (TG*)g.p);
   if (e != cudaSuccess || a.chunks < 2) return e;
-  return launch(c, 2 * c.num_sms, dim3(256),
-                vec ? grad_join_kernel<TG, 4> : grad_join_kernel<TG, 1>, a, (TG*)g.p);
+  // at most one run per chunk crosses into it
+  const int64_t joins = (a.chunks - 1) * ((a.dim + 255) / 256);
+  return launch(c, joins < 6 * c.num_sms ? joins : 6 * c.num_sms, dim3(256),
+                vec ? grad_join_kernel<TG, true> : grad_join_kernel<TG, false>, a, (TG*)g.p);
 }
 
 template <class TD>

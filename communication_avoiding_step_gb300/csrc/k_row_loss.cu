@@ -7,8 +7,9 @@
 // exponential per element and pass, so the bytes of the logits and of the gradient bound
 // them.  All of it is in FP32, rounded once to the logits' type.
 //
-//   Policy loss: g depends on the row alone, so a row is read once.  It is held on chip
-//   between its sum and its gradient (policy_kernel).
+//   Policy loss: g depends on the row alone, so one block reads a row for its sum and at
+//   once again for its gradient: the rows in flight (two per SM) stay in L2 between, and
+//   memory sees one read and one write (policy_kernel).
 //   Preference loss: g depends on every row of both sequences of a pair, which do not fit
 //   on chip, so the rows are read twice (pref_stats_kernel, pref_grad_kernel) with the
 //   pairs' sums between (pref_pair_kernel).
@@ -16,7 +17,6 @@
 // Rows are handled in 16-byte granules of memory, counted from the granule that holds the
 // row's first element, so that rows at any alignment take the same path; the granules that
 // hold elements of other rows too (at most the first and the last) go element by element.
-#include "ptx_async.cuh"
 #include "token_common.cuh"
 
 namespace casgd {
@@ -178,10 +178,16 @@ struct Row {
         whole1((int)((cols + shift) / kV)) {}
   __device__ __forceinline__ int64_t first(int g) const { return (int64_t)g * kV - shift; }
   __device__ __forceinline__ bool whole(int g) const { return g >= whole0 && g < whole1; }
-  // granule g; -inf in the places of other rows' elements
+  // granule g; -inf in the places of other rows' elements.  kLast: not needed again (the
+  // cache may drop it first).
+  template <bool kLast = false>
   __device__ __forceinline__ Granule load(int g) const {
     const T* p = x + first(g);
-    if (whole(g)) return *reinterpret_cast<const Granule*>(p);
+    if (whole(g)) {
+      const uint4* q = reinterpret_cast<const uint4*>(p);
+      const uint4 v = kLast ? __ldcs(q) : *q;
+      return {{v.x, v.y, v.z, v.w}};
+    }
     Granule o = no_granule<T>();
     const int64_t i = first(g);
 #pragma unroll
@@ -202,7 +208,7 @@ __device__ __forceinline__ void put_granule(const Row<T>& r, T* out, bool aligne
   constexpr int kV = Row<T>::kV;
   T* dst = out + r.first(g);
   if (aligned && r.whole(g)) {
-    *reinterpret_cast<Granule*>(dst) = p;
+    __stcs(reinterpret_cast<uint4*>(dst), make_uint4(p.w[0], p.w[1], p.w[2], p.w[3]));
   } else {
     const int64_t i = r.first(g);
 #pragma unroll
@@ -282,7 +288,7 @@ __device__ __forceinline__ void row_grad(const Row<T>& r, T* out, int g0, int g1
     Granule v[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u)
-      if (!zero && i + u * step < g1) v[u] = r.load(i + u * step);
+      if (!zero && i + u * step < g1) v[u] = r.template load<true>(i + u * step);
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const int gr = i + u * step;
@@ -330,6 +336,8 @@ constexpr int kBlock = 256;
 // Up to this many columns a warp takes a row, else a block: a block's two barriers cost
 // more than a warp's longer loop there.
 constexpr int64_t kWarpCols = 2048;
+// Up to this many a block of 256 takes a row of the policy loss, else one of 512.
+constexpr int64_t kBlockCols = 16384;
 
 // Each row's maximum, sum and log probability; kT threads per row.
 template <class T, int kT>
@@ -526,54 +534,19 @@ __device__ __forceinline__ RowLoss policy_row(const PolicyArgs& a, const RowInfo
   return o;
 }
 
-__device__ __forceinline__ void put_row_loss(const PolicyArgs& a, const PolicyWs& w, int64_t t,
-                                             const RowLoss& o) {
-  a.logp[t] = o.lp;
-  w.loss[t] = o.loss;
-  w.kl[t] = o.kl;
-  w.clipped[t] = o.clipped;
-}
-
-// The last of `blocks` blocks to come here adds the rows' terms in a fixed order.  Called
-// by every thread of the block's first kBlock.
-__device__ void policy_sums(const PolicyArgs& a, const PolicyWs& w, unsigned blocks, int bar) {
+// One row per kT threads: its sum, its loss, its gradient.  The last block to finish adds
+// the rows' terms in a fixed order.  Blocks take every gridDim-th row: at kT = 512 two
+// blocks per SM, so that one's loads cover the other's reduction, and few enough rows in
+// flight for L2 to hold them until they are read again.
+template <class T, int kT, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == 512 ? 2 : 4)
+    policy_kernel(PolicyArgs a, PolicyWs w) {
   __shared__ int last;
-  __shared__ double red[3][kBlock / 32];
-  __threadfence();
-  asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(kBlock) : "memory");
-  if (threadIdx.x == 0) last = atomicAdd(&w.ctrl->loss_done, 1u) == blocks - 1;
-  asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(kBlock) : "memory");
-  if (!last) return;
-  __threadfence();
-  double s[3] = {0, 0, 0};
-  for (int64_t t = threadIdx.x; t < a.logits.rows; t += kBlock) {
-    s[0] += __ldcg(&w.loss[t]);
-    s[1] += __ldcg(&w.kl[t]);
-    s[2] += __ldcg(&w.clipped[t]);
-  }
-#pragma unroll
-  for (int e = 0; e < 3; ++e) {
-#pragma unroll
-    for (int h = 16; h > 0; h /= 2) s[e] += __shfl_xor_sync(0xffffffffu, s[e], h);
-    if ((threadIdx.x & 31) == 0) red[e][threadIdx.x >> 5] = s[e];
-  }
-  asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(kBlock) : "memory");
-  if (threadIdx.x < 3) {
-    double v = 0.0;
-    for (int i = 0; i < kBlock / 32; ++i) v += red[threadIdx.x][i];
-    a.stats[threadIdx.x] = (float)v;
-  }
-  if (threadIdx.x == 0) w.ctrl->loss_done = 0;
-}
-
-// Rows too long to be held on chip, and rows short enough for a warp: the row is read,
-// then read again (from L2 or L1) for its gradient.  kT threads per row.
-template <class T, int kT>
-__global__ void __launch_bounds__(kBlock) policy_reread_kernel(PolicyArgs a, PolicyWs w) {
+  __shared__ double red[3][kThreads / 32];
   wait_prior_grid();
   allow_next_grid();
   const int tid = threadIdx.x % kT;
-  constexpr int kRows = kBlock / kT;
+  constexpr int kRows = kThreads / kT;
   const float inv_t = 1.0f / a.temperature, scale = kLog2e * inv_t;
   for (int64_t t = (int64_t)blockIdx.x * kRows + threadIdx.x / kT; t < a.logits.rows;
        t += (int64_t)gridDim.x * kRows) {
@@ -587,292 +560,41 @@ __global__ void __launch_bounds__(kBlock) policy_reread_kernel(PolicyArgs a, Pol
       r = row_max_sum<T, kT>(row, tid, scale);
     }
     const RowLoss o = policy_row(a, f, r, inv_t, scale);
-    if (tid == 0) put_row_loss(a, w, t, o);
+    if (tid == 0) {
+      a.logp[t] = o.lp;
+      w.loss[t] = o.loss;
+      w.kl[t] = o.kl;
+      w.clipped[t] = o.clipped;
+    }
     if (a.grad.p)
-      row_grad(row, static_cast<T*>(a.grad.p) + t * a.grad.ld, tid, row.granules, kT,
-               scale, r, f.target, o.g, f.weight == 0.0f || o.none());
+      row_grad(row, static_cast<T*>(a.grad.p) + t * a.grad.ld, tid, row.granules, kT, scale, r,
+               f.target, o.g, f.weight == 0.0f || o.none());
   }
-  policy_sums(a, w, gridDim.x, 0);
-}
-
-// Rows held on chip.  A cluster of C CTAs takes a row, each CTA a slice of up to
-// kBlock * kQ granules, kQ per thread.  A producer warp copies the slices of the next rows
-// into a ring of three stages with bulk copies and passes the row's scalars along.  The
-// other warps work on two rows in turn: the maximum and sum of the next row's slice, sent
-// as one pair per warp to every CTA of the cluster (distributed shared memory), then, with
-// the pairs of the row before it long arrived, that row's gradient from its stage.  So one
-// read and one write per element, two exponentials, and an exchange per row that nothing
-// waits for.
-constexpr int kStages = 3;
-constexpr int kConsumers = kBlock, kRingThreads = kBlock + 32;
-constexpr int kWarps = kConsumers / 32;
-constexpr int kMaxCluster = 8;
-constexpr int kExchanges = 4;
-constexpr uint64_t kTimeoutNs = 1000000000ull;
-
-struct RingShared {
-  // Four exchanges: a peer sends row i + 4's pairs only after this CTA sent row i + 2's,
-  // which it does after it has read row i's.
-  uint64_t full[kStages], empty[kStages], red[kExchanges];
-  uint64_t pair[kExchanges][kMaxCluster * kWarps];  // (max, sum) of every warp of the cluster
-  RowInfo info[kStages];
-  volatile uint32_t abort;
-};
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
-               ::: "memory");
-}
-// Writes v to the same shared address of CTA `rank` of the cluster and counts its 8 bytes
-// on that CTA's barrier.
-__device__ __forceinline__ void send_pair(uint64_t* dst, uint64_t* bar, uint32_t rank, uint64_t v) {
-  asm volatile(
-      "{\n\t.reg .b32 d, b;\n\t"
-      "mapa.shared::cluster.u32 d, %0, %2;\n\t"
-      "mapa.shared::cluster.u32 b, %1, %2;\n\t"
-      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b64 [d], %3, [b];\n\t}" ::"r"(
-          smem_u32(dst)),
-      "r"(smem_u32(bar)), "r"(rank), "l"(v)
-      : "memory");
-}
-__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-// Bounded wait; false if the phase does not complete in time or the CTA gave up.
-template <bool kCluster>
-__device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity, RingShared* sh,
-                                          Ctrl* ctrl) {
-  if (kCluster ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (true) {
-    if (kCluster ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
-    if (sh->abort) return false;
-    if (globaltimer_ns() - t0 > kTimeoutNs) {
-      sh->abort = 1;
-      atomicOr(&ctrl->status, ST_TIMEOUT);
-      return false;
-    }
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) last = atomicAdd(&w.ctrl->loss_done, 1u) == gridDim.x - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  double s[3] = {0, 0, 0};
+  for (int64_t t = threadIdx.x; t < a.logits.rows; t += kThreads) {
+    s[0] += __ldcg(&w.loss[t]);
+    s[1] += __ldcg(&w.kl[t]);
+    s[2] += __ldcg(&w.clipped[t]);
   }
-}
-
-template <class T, int kQ>
-constexpr size_t ring_bytes() {
-  return (size_t)kStages * kBlock * kQ * 16 + sizeof(RingShared) + 16;
-}
-
-// Blocks per SM: as many as the stages leave shared memory for, up to three.
-template <class T, int kQ>
-constexpr int ring_blocks() {
-  return kQ <= 4 ? 3 : kQ <= 8 ? 2 : 1;
-}
-
-template <class T, int kQ>
-__global__ void __launch_bounds__(kRingThreads, ring_blocks<T, kQ>())
-    policy_kernel(PolicyArgs a, PolicyWs w, int C) {
-  constexpr int kV = Row<T>::kV;
-  extern __shared__ __align__(16) uint8_t ring[];
-  RingShared* sh = reinterpret_cast<RingShared*>(ring + (size_t)kStages * kBlock * kQ * 16);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = C > 1 ? cluster_rank() : 0u;
-  const int64_t cluster = blockIdx.x / C, clusters = gridDim.x / C;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(&sh->full[i], 1);
-      mbar_init(&sh->empty[i], kWarps);
-    }
-    for (int i = 0; i < kExchanges; ++i) mbar_init(&sh->red[i], 1);
-    sh->abort = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+#pragma unroll
+  for (int e = 0; e < 3; ++e) {
+#pragma unroll
+    for (int h = 16; h > 0; h /= 2) s[e] += __shfl_xor_sync(0xffffffffu, s[e], h);
+    if ((threadIdx.x & 31) == 0) red[e][threadIdx.x >> 5] = s[e];
   }
   __syncthreads();
-  cluster_sync();
-  wait_prior_grid();
-  allow_next_grid();
-  const float inv_t = 1.0f / a.temperature, scale = kLog2e * inv_t;
-  const T* logits = static_cast<const T*>(a.logits.p);
-
-  if (warp == kWarps) {
-    // ---------------------------------------------------------------- producer warp
-    int stage = 0;
-    uint32_t phase = 0, issued = 0, last_par = 0;
-    bool ok = true;
-    for (int64_t t0 = cluster; t0 < a.logits.rows && ok; t0 += 32 * clusters) {
-      // the scalars of the next 32 rows, one row per lane
-      RowInfo mine{-1, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-      const int64_t tl = t0 + lane * clusters;
-      if (tl < a.logits.rows) {
-        if (load_info(a, tl, mine) && rank == 0) set_status(w.ctrl, ST_BAD_INDEX);
-        if (mine.target >= 0) mine.xt = Elem<T>::get(logits[tl * a.logits.ld + mine.target]);
-      }
-      for (int i = 0; i < 32; ++i) {
-        const int64_t t = t0 + i * clusters;
-        if (t >= a.logits.rows) break;
-        ok = __shfl_sync(0xffffffffu,
-                         lane == 0 ? (int)ring_wait<false>(&sh->empty[stage], phase ^ 1u, sh,
-                                                           w.ctrl) : 0, 0) != 0;
-        if (!ok) break;
-        const int64_t target = __shfl_sync(0xffffffffu, mine.target, i);
-        if (lane == i) sh->info[stage] = mine;
-        uint32_t bytes = 0;
-        int b0 = 0, c0 = 0;
-        const Row<T> row(logits + t * a.logits.ld, a.logits.cols);
-        T* buf = reinterpret_cast<T*>(ring + (size_t)stage * kBlock * kQ * 16);
-        if (target >= 0) {
-          const int per = (row.granules + C - 1) / C;
-          c0 = (int)rank * per;
-          const int c1 = c0 + per < row.granules ? c0 + per : row.granules;
-          if (c0 < c1) {
-            // granules shared with other rows: their elements one by one (lanes 0-15)
-            b0 = row.whole(c0) ? c0 : c0 + 1;
-            int b1 = c1 > b0 && !row.whole(c1 - 1) ? c1 - 1 : c1;
-            if (b1 < b0) b1 = b0;
-            const int eg = lane < 8 ? c0 : c1 - 1;
-            const int e = lane & 7;
-            if (lane < 16 && e < kV && (lane < 8 ? b0 > c0 : b1 < c1 && b1 >= b0)) {
-              const int64_t el = row.first(eg) + e;
-              if (el >= 0 && el < row.n) buf[(eg - c0) * kV + e] = row.x[el];
-            }
-            bytes = (uint32_t)((b1 - b0) * 16);
-          }
-        }
-        __syncwarp();
-        if (lane == 0) {
-          if (bytes) {
-            mbar_expect_tx(&sh->full[stage], bytes);
-            bulk_load(buf + (b0 - c0) * kV, row.x + row.first(b0), bytes, &sh->full[stage]);
-            issued |= 1u << stage;
-            last_par = (last_par & ~(1u << stage)) | (phase << stage);
-          } else {  // (an earlier copy into this stage has landed: its row was consumed)
-            mbar_arrive(&sh->full[stage]);
-            issued &= ~(1u << stage);
-          }
-        }
-        if (++stage == kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      }
-    }
-    if (lane == 0)  // every copy has landed before the CTA may exit
-      for (int st = 0; st < kStages; ++st)
-        if (issued & (1u << st)) {
-          const uint64_t t0 = globaltimer_ns();
-          while (!mbar_try_wait(&sh->full[st], (last_par >> st) & 1u) &&
-                 globaltimer_ns() - t0 < kTimeoutNs) {
-          }
-        }
-    __syncwarp();
-  } else {
-    // ---------------------------------------------------------------- the other warps
-    const Granule* bufs = reinterpret_cast<const Granule*>(ring);
-    // stage and phase of the next row to sum, exchange numbers of the next row to sum and
-    // of the next to write
-    int stage = 0;
-    uint32_t phase = 0, sent = 0, taken = 0;
-    auto slice = [&](const Row<T>& row, int& c0) {
-      const int per = (row.granules + C - 1) / C;
-      c0 = (int)rank * per;
-      return c0 + per < row.granules ? per : c0 < row.granules ? row.granules - c0 : 0;
-    };
-    auto sum_row = [&](int64_t t) -> bool {  // the next stage's row: sum it, send the pairs
-      if (!__all_sync(0xffffffffu, ring_wait<false>(&sh->full[stage], phase, sh, w.ctrl)))
-        return false;
-      if (sh->info[stage].target >= 0) {
-        const Row<T> row(logits + t * a.logits.ld, a.logits.cols);
-        int c0;
-        const int n = slice(row, c0);
-        Granule p[kQ];
-#pragma unroll
-        for (int q = 0; q < kQ; ++q) {
-          const int i = threadIdx.x + q * kBlock;
-          p[q] = i < n ? bufs[stage * kBlock * kQ + i] : no_granule<T>();
-          if (i < n && !row.whole(c0 + i)) {
-            const int64_t el = row.first(c0 + i);
-#pragma unroll
-            for (int j = 0; j < kV; ++j)
-              if (el + j < 0 || el + j >= row.n) set_element(p[q], j, lowest<T>());
-          }
-        }
-        const MaxSum wp = join_lanes<32>(granules_max_sum<T, kQ>(p, scale));
-        uint64_t* bar = &sh->red[sent % kExchanges];
-        if (threadIdx.x == 0) mbar_expect_tx(bar, (uint32_t)(C * kWarps * 8));
-        if (lane < C)
-          send_pair(sh->pair[sent % kExchanges] + rank * kWarps + warp, bar, lane,
-                    (uint64_t)__float_as_uint(wp.s) << 32 | __float_as_uint(wp.m));
-        ++sent;
-      }
-      if (++stage == kStages) {
-        stage = 0;
-        phase ^= 1u;
-      }
-      return true;
-    };
-    bool ok = cluster < a.logits.rows && sum_row(cluster);
-    int ws = 0;  // stage of the row to write
-    for (int64_t t = cluster; t < a.logits.rows && ok; t += clusters) {
-      if (t + clusters < a.logits.rows) ok = sum_row(t + clusters);
-      if (!ok) break;
-      const RowInfo f = sh->info[ws];
-      MaxSum r{0.0f, 1.0f};
-      if (f.target >= 0) {
-        const int e = taken % kExchanges;
-        ok = __all_sync(0xffffffffu, ring_wait<true>(&sh->red[e], (taken / kExchanges) & 1u, sh,
-                                                     w.ctrl));
-        if (!ok) break;
-        ++taken;
-        MaxSum x{-INFINITY, 0.0f}, y{-INFINITY, 0.0f};
-        if (lane < C * kWarps) {
-          const uint64_t v = sh->pair[e][lane];
-          x = {__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32))};
-        }
-        if (lane + 32 < C * kWarps) {
-          const uint64_t v = sh->pair[e][lane + 32];
-          y = {__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32))};
-        }
-        r = join_lanes<32>(join(x, y));
-      }
-      const RowLoss o = policy_row(a, f, r, inv_t, scale);
-      if (rank == 0 && threadIdx.x == 0) put_row_loss(a, w, t, o);
-      if (a.grad.p) {
-        const Row<T> row(logits + t * a.logits.ld, a.logits.cols);
-        int c0;
-        const int n = slice(row, c0);
-        T* out = static_cast<T*>(a.grad.p) + t * a.grad.ld;
-        const bool al = same_phase(row.x, out), zero = f.weight == 0.0f || o.none();
-        const float k = -o.g / r.s;
-        const Granule* buf = bufs + ws * kBlock * kQ;
-        // the granule that holds the target is set by the thread that stores it
-        const int tg = zero ? -1 : (int)((f.target + row.shift) / kV) - c0;
-#pragma unroll 4
-        for (int i = threadIdx.x; i < n; i += kBlock) {
-          const Granule v = zero ? Granule{{0u, 0u, 0u, 0u}}
-                                 : softmax_part<T>(buf[i], scale, r.m, k);
-          put_granule(row, out, al, c0 + i, v);
-          if (i == tg) out[f.target] = Elem<T>::put(target_grad(o.g, f.xt, r, scale));
-        }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->empty[ws]);
-      ws = ws + 1 == kStages ? 0 : ws + 1;
-    }
-    if (rank == 0) policy_sums(a, w, (unsigned)clusters, 1);
+  if (threadIdx.x < 3) {
+    double v = 0.0;
+    for (int i = 0; i < kThreads / 32; ++i) v += red[threadIdx.x][i];
+    a.stats[threadIdx.x] = (float)v;
   }
-  __syncwarp();
-  cluster_sync();  // no CTA leaves while another may still write to its shared memory
+  if (threadIdx.x == 0) w.ctrl->loss_done = 0;
 }
 
 template <class... P, class... A>
@@ -914,48 +636,16 @@ cudaError_t pref_by_width(const PrefArgs& p, const PrefWs& w, Ctx& c) {
   return p.logits.cols <= kWarpCols ? pref_typed<T, 32>(p, w, c) : pref_typed<T, kBlock>(p, w, c);
 }
 
-template <class T, int kQ>
-cudaError_t policy_ring(const PolicyArgs& p, const PolicyWs& w, int C, Ctx& c) {
-  const auto fn = policy_kernel<T, kQ>;
-  const size_t smem = ring_bytes<T, kQ>();
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)C;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.blockDim = dim3(kRingThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = c.stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cfg.gridDim = dim3((unsigned)C);
-  int fit = 0;  // clusters that fit the GPU at once: one wave, each taking every fit-th row
-  e = cudaOccupancyMaxActiveClusters(&fit, fn, &cfg);
-  if (e != cudaSuccess) return e;
-  if (fit < 1) return cudaErrorInvalidConfiguration;
-  cfg.gridDim = dim3((unsigned)C * blocks_for(p.logits.rows, fit));
-  add_pdl_attr(c, cfg, attr);
-  ++c.launches;
-  return cudaLaunchKernelEx(&cfg, fn, p, w, C);
-}
-
 template <class T>
 cudaError_t policy_typed(const PolicyArgs& p, const PolicyWs& w, Ctx& c) {
-  constexpr int kV = 16 / sizeof(T);
-  constexpr int kSmall = 16 / kV, kLarge = 64 / kV;  // 16 or 64 elements per thread
   const int64_t rows = p.logits.rows;
-  const int64_t granules = (p.logits.cols + kV - 1) / kV + 1;  // at most, at any alignment
-  if (p.logits.cols <= kWarpCols || rows == 0)
-    return launch(c, blocks_for((rows + 7) / 8, 1 << 20), kBlock, policy_reread_kernel<T, 32>, p,
+  if (p.logits.cols <= kWarpCols)
+    return launch(c, blocks_for((rows + 7) / 8, 4 * c.num_sms), kBlock,
+                  policy_kernel<T, 32, kBlock>, p, w);
+  if (p.logits.cols <= kBlockCols)
+    return launch(c, blocks_for(rows, 4 * c.num_sms), kBlock, policy_kernel<T, kBlock, kBlock>, p,
                   w);
-  for (int C = 1; C <= kMaxCluster; C *= 2)
-    if (granules <= (int64_t)C * kBlock * kSmall && (C == 1 || rows * C <= 8 * c.num_sms))
-      return policy_ring<T, kSmall>(p, w, C, c);
-  for (int C = 1; C <= kMaxCluster; C *= 2)
-    if (granules <= (int64_t)C * kBlock * kLarge) return policy_ring<T, kLarge>(p, w, C, c);
-  return launch(c, blocks_for(rows, 1 << 20), kBlock, policy_reread_kernel<T, kBlock>, p, w);
+  return launch(c, blocks_for(rows, 2 * c.num_sms), 512, policy_kernel<T, 512, 512>, p, w);
 }
 
 }  // namespace

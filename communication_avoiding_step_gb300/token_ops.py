@@ -25,9 +25,10 @@ _DTYPES = {torch.float32: CASGD_F32, torch.bfloat16: CASGD_BF16, torch.float16: 
 
 # (Pointers go to ctypes as plain integers, and each tensor is looked at once: the smallest
 # calls take as long as their Python does.)
-def _stream(stream) -> int:
+def _stream(stream, ws) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # torch.cuda.current_stream(ws.device).cuda_stream, without making a Stream object
+        return torch._C._cuda_getCurrentRawStream(ws.get_device())
     return stream.cuda_stream
 
 
@@ -78,7 +79,7 @@ def _workspace(size_call: str, *args, device="cuda", stream=None) -> torch.Tenso
     nbytes = C.c_size_t(0)
     _check(getattr(load(), size_call)(*args, C.byref(nbytes)), size_call)
     ws = torch.empty(nbytes.value, dtype=torch.uint8, device=device)
-    _check(load().casgd_workspace_init(ws.data_ptr(), ws.numel(), _stream(stream)),
+    _check(load().casgd_workspace_init(ws.data_ptr(), ws.numel(), _stream(stream, ws)),
            "casgd_workspace_init")
     return ws
 
@@ -105,7 +106,7 @@ def embed(table: torch.Tensor, tokens: torch.Tensor, out: torch.Tensor, ws: torc
     if o.rows != i.count or o.cols != t.cols:
         raise ValueError(f"out must be {i.count} x {t.cols}, is {o.rows} x {o.cols}")
     _check(load().casgd_embed(C.byref(t), C.byref(i), scale, padding_id, C.byref(o), *_ws(ws),
-                              _stream(stream)), "casgd_embed")
+                              _stream(stream, ws)), "casgd_embed")
     return out
 
 
@@ -120,7 +121,7 @@ def embed_grad(dout: torch.Tensor, tokens: torch.Tensor, grad: torch.Tensor, ws:
         raise ValueError(f"dout must be {i.count} x {g.cols}, is {d.rows} x {d.cols}")
     _check(load().casgd_embed_grad(C.byref(d), C.byref(i), scale, padding_id,
                                    1 if accumulate else 0, C.byref(g), *_ws(ws),
-                                   _stream(stream)), "casgd_embed_grad")
+                                   _stream(stream, ws)), "casgd_embed_grad")
     return grad
 
 
@@ -161,7 +162,7 @@ def group_workspace(x: torch.Tensor, w: torch.Tensor, y: torch.Tensor,
 
 def _group_call(name, x, w, y, offsets, ws, stream):
     g = _group(x, w, y, offsets)
-    _check(getattr(load(), name)(C.byref(g), *_ws(ws), _stream(stream)), name)
+    _check(getattr(load(), name)(C.byref(g), *_ws(ws), _stream(stream, ws)), name)
 
 
 def group_product(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, y: torch.Tensor,
@@ -242,7 +243,7 @@ def preference_loss(logits: torch.Tensor, targets: torch.Tensor, seq_offsets: to
         C.byref(PreferenceParams(beta, kind, smoothing, 1 if mean else 0, grad_scale)),
         _vector(out.loss, "out.loss", torch.float32, 1),
         _vector(out.margin, "out.margin", torch.float32, pairs),
-        _vector(out.logp, "out.logp", torch.float32, 2 * pairs), g, *_ws(ws), _stream(stream)),
+        _vector(out.logp, "out.logp", torch.float32, 2 * pairs), g, *_ws(ws), _stream(stream, ws)),
         "casgd_preference_loss")
     return out
 
@@ -268,5 +269,5 @@ def policy_loss(logits: torch.Tensor, targets: torch.Tensor, weights: torch.Tens
         _vector(adv, "adv", f32, n),
         C.byref(PolicyParams(kl, clip_low, clip_high, temperature, grad_scale)),
         _vector(out.stats, "out.stats", f32, 3), _vector(out.logp, "out.logp", f32, n), g,
-        *_ws(ws), _stream(stream)), "casgd_policy_loss")
+        *_ws(ws), _stream(stream, ws)), "casgd_policy_loss")
     return out
