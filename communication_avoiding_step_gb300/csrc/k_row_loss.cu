@@ -7,16 +7,20 @@
 // exponential per element and pass, so the bytes of the logits and of the gradient bound
 // them.  All of it is in FP32, rounded once to the logits' type.
 //
-//   Policy loss: g depends on the row alone, so one block reads a row for its sum and at
-//   once again for its gradient: the rows in flight (two per SM) stay in L2 between, and
-//   memory sees one read and one write (policy_kernel).
+//   Policy loss: g depends on the row alone, so a block reads a row for its sum and at
+//   once again for its gradient: the rows in flight stay in L2 between, and memory sees
+//   one read and one write.
 //   Preference loss: g depends on every row of both sequences of a pair, which do not fit
-//   on chip, so the rows are read twice (pref_stats_kernel, pref_grad_kernel) with the
-//   pairs' sums between (pref_pair_kernel).
+//   on chip, so one launch reads every row for its sum, one adds up the pairs, and one
+//   reads the rows again for the gradient, in the opposite order, so that what L2 still
+//   holds comes first.
+// Rows wider than kWarpCols go through stream_kernel, a ring of bulk copies per block;
+// shorter ones take a warp each (warp kernels), without shared memory.
 //
 // Rows are handled in 16-byte granules of memory, counted from the granule that holds the
 // row's first element, so that rows at any alignment take the same path; the granules that
 // hold elements of other rows too (at most the first and the last) go element by element.
+#include "ptx_async.cuh"
 #include "token_common.cuh"
 
 namespace casgd {
@@ -178,21 +182,14 @@ struct Row {
         whole1((int)((cols + shift) / kV)) {}
   __device__ __forceinline__ int64_t first(int g) const { return (int64_t)g * kV - shift; }
   __device__ __forceinline__ bool whole(int g) const { return g >= whole0 && g < whole1; }
-  // granule g; -inf in the places of other rows' elements.  kLast: not needed again (the
-  // cache may drop it first).
-  template <bool kLast = false>
+  // granule g; -inf in the places of other rows' elements
   __device__ __forceinline__ Granule load(int g) const {
-    const T* p = x + first(g);
-    if (whole(g)) {
-      const uint4* q = reinterpret_cast<const uint4*>(p);
-      const uint4 v = kLast ? __ldcs(q) : *q;
-      return {{v.x, v.y, v.z, v.w}};
-    }
-    Granule o = no_granule<T>();
     const int64_t i = first(g);
+    if (whole(g)) return *reinterpret_cast<const Granule*>(x + i);
+    Granule o = no_granule<T>();
 #pragma unroll
     for (int e = 0; e < kV; ++e)
-      if (i + e >= 0 && i + e < n) set_element(o, e, p[e]);
+      if (i + e >= 0 && i + e < n) set_element(o, e, x[i + e]);
     return o;
   }
 };
@@ -201,6 +198,9 @@ template <class T>
 __device__ __forceinline__ bool same_phase(const T* a, const T* b) {
   return ((reinterpret_cast<uintptr_t>(a) ^ reinterpret_cast<uintptr_t>(b)) & 15) == 0;
 }
+__device__ __forceinline__ void store_streamed(void* dst, const Granule& p) {
+  __stcs(static_cast<uint4*>(dst), make_uint4(p.w[0], p.w[1], p.w[2], p.w[3]));
+}
 // Granule g of a gradient row (element 0 at `out`), laid over the granules of `r`.
 template <class T>
 __device__ __forceinline__ void put_granule(const Row<T>& r, T* out, bool aligned, int g,
@@ -208,7 +208,7 @@ __device__ __forceinline__ void put_granule(const Row<T>& r, T* out, bool aligne
   constexpr int kV = Row<T>::kV;
   T* dst = out + r.first(g);
   if (aligned && r.whole(g)) {
-    __stcs(reinterpret_cast<uint4*>(dst), make_uint4(p.w[0], p.w[1], p.w[2], p.w[3]));
+    store_streamed(dst, p);
   } else {
     const int64_t i = r.first(g);
 #pragma unroll
@@ -233,37 +233,24 @@ __device__ __forceinline__ Granule softmax_part(const Granule& x, float scale, f
   return o;
 }
 
-// Maximum and sum of a row by kT threads (a warp, or a block of kT); every thread gets
-// them.  Two groups of granules take turns: one is loaded while the other is summed.
-template <class T, int kT>
-__device__ MaxSum row_max_sum(const Row<T>& r, int tid, float scale) {
+// Maximum and sum of a row by a warp; every lane gets them.
+template <class T>
+__device__ __forceinline__ MaxSum warp_max_sum(const Row<T>& r, int lane, float scale) {
   constexpr int kU = 4;
   MaxSum acc{-INFINITY, 0.0f};
-  Granule cur[kU], next[kU];
-  auto fetch = [&](Granule(&p)[kU], int g0) {
+  int g = lane;
+  for (; g + 32 * (kU - 1) < r.granules; g += 32 * kU) {
+    Granule p[kU];
 #pragma unroll
-    for (int u = 0; u < kU; ++u)
-      p[u] = g0 + u * kT < r.granules ? r.load(g0 + u * kT) : no_granule<T>();
-  };
-  fetch(cur, tid);
-  for (int g0 = tid; g0 < r.granules; g0 += kT * kU) {
-    const bool more = g0 + kT * kU < r.granules;
-    if (more) fetch(next, g0 + kT * kU);
-    acc = join(acc, granules_max_sum<T, kU>(cur, scale));
-    if (more) {
-#pragma unroll
-      for (int u = 0; u < kU; ++u) cur[u] = next[u];
-    }
+    for (int u = 0; u < kU; ++u) p[u] = r.load(g + 32 * u);
+    acc = join(acc, granules_max_sum<T, kU>(p, scale));
   }
-  acc = join_lanes<32>(acc);
-  if (kT > 32) {
-    __shared__ MaxSum part[kT / 32];
-    __syncthreads();
-    if ((tid & 31) == 0) part[tid >> 5] = acc;
-    __syncthreads();
-    acc = join_lanes<kT / 32>(part[tid & (kT / 32 - 1)]);
+#pragma unroll 1
+  for (; g < r.granules; g += 32) {
+    const Granule p[1] = {r.load(g)};
+    acc = join(acc, granules_max_sum<T, 1>(p, scale));
   }
-  return acc;
+  return join_lanes<32>(acc);
 }
 
 // The target's log probability.
@@ -276,38 +263,21 @@ __device__ __forceinline__ float target_grad(float g, float xt, MaxSum r, float 
   return g * (1.0f - fast_exp2(fmaf(xt, scale, -r.m)) / r.s);
 }
 
-// Writes g * (onehot - softmax), or zeros, for granules g0, g0 + step, .. below g1.
+// Writes g * (onehot - softmax), or zeros, to a row by a warp.
 template <class T>
-__device__ __forceinline__ void row_grad(const Row<T>& r, T* out, int g0, int g1, int step,
-                                         float scale, MaxSum ms, int64_t target,
-                                         float g, bool zero) {
-  constexpr int kV = Row<T>::kV, kU = 4;
+__device__ __forceinline__ void warp_grad(const Row<T>& r, T* out, int lane, float scale,
+                                          MaxSum ms, int64_t target, float g, bool zero) {
   const bool al = same_phase(r.x, out);
   const float k = -g / ms.s;
-  for (int i = g0; i < g1; i += step * kU) {
-    Granule v[kU];
-#pragma unroll
-    for (int u = 0; u < kU; ++u)
-      if (!zero && i + u * step < g1) v[u] = r.template load<true>(i + u * step);
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int gr = i + u * step;
-      if (gr >= g1) break;
-      Granule o{{0u, 0u, 0u, 0u}};
-      if (!zero) {
-        o = softmax_part<T>(v[u], scale, ms.m, k);
-        const int64_t t = target - r.first(gr);
-        if (t >= 0 && t < kV) {
-#pragma unroll
-          for (int e = 0; e < kV; ++e)
-            if (t == e)
-              set_element(o, e, Elem<T>::put(target_grad(
-                                    g, Elem<T>::get(element<T>(v[u], e)), ms, scale)));
-        }
-      }
-      put_granule(r, out, al, gr, o);
-    }
-  }
+  const int tg = zero ? -1 : (int)((target + r.shift) / Row<T>::kV);
+  const bool mine = tg >= 0 && tg % 32 == lane;
+  const float xt = mine ? Elem<T>::get(r.x[target]) : 0.0f;  // (before the row is written)
+#pragma unroll 2
+  for (int i = lane; i < r.granules; i += 32)
+    put_granule(r, out, al, i, zero ? Granule{{0u, 0u, 0u, 0u}}
+                                    : softmax_part<T>(r.load(i), scale, ms.m, k));
+  // the lane that stored the target's granule sets the target
+  if (mine) out[target] = Elem<T>::put(target_grad(g, xt, ms, scale));
 }
 
 // ------------------------------------------------------------------ preference loss
@@ -333,36 +303,36 @@ struct PrefWs {
 };
 
 constexpr int kBlock = 256;
-// Up to this many columns a warp takes a row, else a block: a block's two barriers cost
-// more than a warp's longer loop there.
+// Up to this many columns a warp takes a row, else a block: a block's barriers and copies
+// cost more than a warp's longer loop there.
 constexpr int64_t kWarpCols = 2048;
-// Up to this many a block of 256 takes a row of the policy loss, else one of 512.
-constexpr int64_t kBlockCols = 16384;
 
-// Each row's maximum, sum and log probability; kT threads per row.
-template <class T, int kT>
-__global__ void __launch_bounds__(kBlock, 4) pref_stats_kernel(PrefArgs a, PrefWs w) {
+__device__ __forceinline__ void put_stats(const PrefWs& w, int64_t t, MaxSum r, float lp) {
+  w.m[t] = r.m;
+  w.s[t] = r.s;
+  w.lp[t] = lp;
+  w.coef[t] = 0.0f;  // pref_pair_kernel sets that of the rows of a sequence
+}
+
+template <class T>
+__global__ void __launch_bounds__(kBlock, 3) pref_stats_warp_kernel(PrefArgs a, PrefWs w) {
   wait_prior_grid();
   allow_next_grid();
-  const int tid = threadIdx.x % kT;
-  constexpr int kRows = kBlock / kT;
-  for (int64_t t = (int64_t)blockIdx.x * kRows + threadIdx.x / kT; t < a.logits.rows;
-       t += (int64_t)gridDim.x * kRows) {
-    const int64_t target = a.targets.at(t);
-    const bool bad = target >= a.logits.cols;
-    if (bad && tid == 0) set_status(w.ctrl, ST_BAD_INDEX);
-    if (target < 0 || bad) {
-      if (tid == 0) w.coef[t] = w.lp[t] = w.m[t] = w.s[t] = 0.0f;
-      continue;
-    }
+  const int lane = threadIdx.x & 31;
+  const int64_t t = ((int64_t)blockIdx.x * kBlock + threadIdx.x) >> 5;
+  if (t >= a.logits.rows) return;
+  const int64_t target = a.targets.at(t);
+  const bool bad = target >= a.logits.cols;
+  MaxSum r{0.0f, 0.0f};
+  float lp = 0.0f;
+  if (target >= 0 && !bad) {
     const Row<T> row(static_cast<const T*>(a.logits.p) + t * a.logits.ld, a.logits.cols);
-    const MaxSum r = row_max_sum<T, kT>(row, tid, kLog2e);
-    if (tid == 0) {
-      w.m[t] = r.m;
-      w.s[t] = r.s;
-      w.coef[t] = 0.0f;
-      w.lp[t] = log_prob(Elem<T>::get(row.x[target]), r, kLog2e);
-    }
+    r = warp_max_sum<T>(row, lane, kLog2e);
+    lp = log_prob(Elem<T>::get(row.x[target]), r, kLog2e);
+  }
+  if (lane == 0) {
+    if (bad) set_status(w.ctrl, ST_BAD_INDEX);
+    put_stats(w, t, r, lp);
   }
 }
 
@@ -455,29 +425,18 @@ __global__ void __launch_bounds__(kBlock) pref_pair_kernel(PrefArgs a, PrefWs w)
   }
 }
 
-// The gradient.  kT threads take a segment of 4 granules each of a row; segments (rows for
-// warps) are dealt to the blocks in descending order, so that the rows read last by
-// pref_stats_kernel, still in L2, come first.
-template <class T, int kT>
-__global__ void __launch_bounds__(kBlock, 5) pref_grad_kernel(PrefArgs a, PrefWs w, int64_t segs) {
+template <class T>
+__global__ void __launch_bounds__(kBlock, 3) pref_grad_warp_kernel(PrefArgs a, PrefWs w) {
   wait_prior_grid();
   allow_next_grid();
-  const int tid = threadIdx.x % kT;
-  constexpr int kItems = kBlock / kT, kSeg = kT * 4;
-  const int64_t items = a.logits.rows * segs;
-  for (int64_t it = (int64_t)blockIdx.x * kItems + threadIdx.x / kT; it < items;
-       it += (int64_t)gridDim.x * kItems) {
-    const int64_t rev = items - 1 - it;
-    const int64_t t = rev / segs, seg = rev - t * segs;
-    const int64_t target = a.targets.at(t);
-    const float g = w.coef[t];
-    const MaxSum ms{w.m[t], w.s[t]};
-    const bool zero = target < 0 || target >= a.logits.cols || g == 0.0f;
-    const Row<T> row(static_cast<const T*>(a.logits.p) + t * a.logits.ld, a.logits.cols);
-    const int g1 = seg == segs - 1 ? row.granules : (int)(seg + 1) * kSeg;
-    row_grad(row, static_cast<T*>(a.grad.p) + t * a.grad.ld, (int)seg * kSeg + tid, g1, kT, kLog2e, ms,
-             target, g, zero);
-  }
+  const int64_t i = ((int64_t)blockIdx.x * kBlock + threadIdx.x) >> 5;
+  if (i >= a.logits.rows) return;
+  const int64_t t = a.logits.rows - 1 - i, target = a.targets.at(t);
+  const float g = w.coef[t];
+  const Row<T> row(static_cast<const T*>(a.logits.p) + t * a.logits.ld, a.logits.cols);
+  warp_grad(row, static_cast<T*>(a.grad.p) + t * a.grad.ld, threadIdx.x & 31, kLog2e,
+            {w.m[t], w.s[t]}, target, g,
+            target < 0 || target >= a.logits.cols || g == 0.0f);
 }
 
 // ------------------------------------------------------------------ policy loss
@@ -486,7 +445,7 @@ struct PolicyWs {
   float *loss, *kl, *clipped;  // per row
 };
 
-// What the loss reads of a row beside its logits.
+// What the policy loss reads of a row beside its logits.
 struct RowInfo {
   int64_t target;  // -1: masked
   float xt, weight, old_logp, ref_logp, adv;
@@ -534,50 +493,28 @@ __device__ __forceinline__ RowLoss policy_row(const PolicyArgs& a, const RowInfo
   return o;
 }
 
-// One row per kT threads: its sum, its loss, its gradient.  The last block to finish adds
-// the rows' terms in a fixed order.  Blocks take every gridDim-th row: at kT = 512 two
-// blocks per SM, so that one's loads cover the other's reduction, and few enough rows in
-// flight for L2 to hold them until they are read again.
-template <class T, int kT, int kThreads>
-__global__ void __launch_bounds__(kThreads, kThreads == 512 ? 2 : 4)
-    policy_kernel(PolicyArgs a, PolicyWs w) {
+__device__ __forceinline__ void put_row_loss(const PolicyArgs& a, const PolicyWs& w, int64_t t,
+                                             const RowLoss& o) {
+  a.logp[t] = o.lp;
+  w.loss[t] = o.loss;
+  w.kl[t] = o.kl;
+  w.clipped[t] = o.clipped;
+}
+
+// The last block to come here adds the rows' terms in a fixed order.  Called by the first
+// kBlock threads of every block (named barrier 1).
+__device__ void policy_sums(const PolicyArgs& a, const PolicyWs& w) {
   __shared__ int last;
-  __shared__ double red[3][kThreads / 32];
-  wait_prior_grid();
-  allow_next_grid();
-  const int tid = threadIdx.x % kT;
-  constexpr int kRows = kThreads / kT;
-  const float inv_t = 1.0f / a.temperature, scale = kLog2e * inv_t;
-  for (int64_t t = (int64_t)blockIdx.x * kRows + threadIdx.x / kT; t < a.logits.rows;
-       t += (int64_t)gridDim.x * kRows) {
-    RowInfo f;
-    if (load_info(a, t, f) && tid == 0) set_status(w.ctrl, ST_BAD_INDEX);
-    const Row<T> row(static_cast<const T*>(a.logits.p) + t * a.logits.ld, a.logits.cols);
-    MaxSum r{0.0f, 1.0f};
-    f.xt = 0.0f;
-    if (f.target >= 0) {
-      f.xt = Elem<T>::get(row.x[f.target]);
-      r = row_max_sum<T, kT>(row, tid, scale);
-    }
-    const RowLoss o = policy_row(a, f, r, inv_t, scale);
-    if (tid == 0) {
-      a.logp[t] = o.lp;
-      w.loss[t] = o.loss;
-      w.kl[t] = o.kl;
-      w.clipped[t] = o.clipped;
-    }
-    if (a.grad.p)
-      row_grad(row, static_cast<T*>(a.grad.p) + t * a.grad.ld, tid, row.granules, kT, scale, r,
-               f.target, o.g, f.weight == 0.0f || o.none());
-  }
+  __shared__ double red[3][kBlock / 32];
+  auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(kBlock) : "memory"); };
   __threadfence();
-  __syncthreads();
+  meet();
   if (threadIdx.x == 0) last = atomicAdd(&w.ctrl->loss_done, 1u) == gridDim.x - 1;
-  __syncthreads();
+  meet();
   if (!last) return;
   __threadfence();
   double s[3] = {0, 0, 0};
-  for (int64_t t = threadIdx.x; t < a.logits.rows; t += kThreads) {
+  for (int64_t t = threadIdx.x; t < a.logits.rows; t += kBlock) {
     s[0] += __ldcg(&w.loss[t]);
     s[1] += __ldcg(&w.kl[t]);
     s[2] += __ldcg(&w.clipped[t]);
@@ -588,13 +525,343 @@ __global__ void __launch_bounds__(kThreads, kThreads == 512 ? 2 : 4)
     for (int h = 16; h > 0; h /= 2) s[e] += __shfl_xor_sync(0xffffffffu, s[e], h);
     if ((threadIdx.x & 31) == 0) red[e][threadIdx.x >> 5] = s[e];
   }
-  __syncthreads();
+  meet();
   if (threadIdx.x < 3) {
     double v = 0.0;
-    for (int i = 0; i < kThreads / 32; ++i) v += red[threadIdx.x][i];
+    for (int i = 0; i < kBlock / 32; ++i) v += red[threadIdx.x][i];
     a.stats[threadIdx.x] = (float)v;
   }
   if (threadIdx.x == 0) w.ctrl->loss_done = 0;
+}
+
+template <class T>
+__global__ void __launch_bounds__(kBlock, 3) policy_warp_kernel(PolicyArgs a, PolicyWs w) {
+  wait_prior_grid();
+  allow_next_grid();
+  const int lane = threadIdx.x & 31;
+  const float inv_t = 1.0f / a.temperature, scale = kLog2e * inv_t;
+  for (int64_t t = ((int64_t)blockIdx.x * kBlock + threadIdx.x) >> 5; t < a.logits.rows;
+       t += (int64_t)gridDim.x * (kBlock / 32)) {
+    RowInfo f;
+    const bool bad = load_info(a, t, f);
+    const Row<T> row(static_cast<const T*>(a.logits.p) + t * a.logits.ld, a.logits.cols);
+    MaxSum r{0.0f, 1.0f};
+    f.xt = 0.0f;
+    if (f.target >= 0) {
+      f.xt = Elem<T>::get(row.x[f.target]);
+      r = warp_max_sum<T>(row, lane, scale);
+    }
+    const RowLoss o = policy_row(a, f, r, inv_t, scale);
+    if (lane == 0) {
+      if (bad) set_status(w.ctrl, ST_BAD_INDEX);
+      put_row_loss(a, w, t, o);
+    }
+    if (a.grad.p)
+      warp_grad(row, static_cast<T*>(a.grad.p) + t * a.grad.ld, lane, scale, r, f.target, o.g,
+                f.weight == 0.0f || o.none());
+  }
+  policy_sums(a, w);
+}
+
+// ------------------------------------------------------------------ rows through a ring
+// One block per row.  A producer warp copies the row's whole granules, 16 KB at a time,
+// into a ring of stages with bulk copies, once for the sum and once more for the gradient,
+// and runs ahead into the next rows, so that copies stay in flight while the block reduces
+// a row or waits for its stores; the scalars of a row travel with its first stage.  The
+// other eight warps sum a stage or turn it into gradients.  Granules shared with other rows
+// (at most the first and the last) are read and written element by element by two threads.
+enum StreamMode { STREAM_STATS, STREAM_GRAD, STREAM_POLICY };
+constexpr int kStages = 6;
+constexpr int kU = 4;                       // granules per thread and stage
+constexpr int kStageGranules = kBlock * kU;
+constexpr int kWarps = kBlock / 32;
+constexpr int kStreamThreads = kBlock + 32;
+constexpr uint64_t kTimeoutNs = 1000000000ull;
+
+struct StreamShared {
+  uint64_t full[kStages], empty[kStages];
+  RowInfo info[kStages];
+  MaxSum part[kWarps];
+  MaxSum sum;
+  RowLoss loss;
+  volatile uint32_t abort;
+};
+constexpr size_t kStreamSmem = (size_t)kStages * kStageGranules * 16 + sizeof(StreamShared);
+
+// Bounded wait by a whole warp; false if the phase does not complete in time or the block
+// gave up.
+__device__ __forceinline__ bool stage_wait(uint64_t* bar, uint32_t parity, StreamShared* sh,
+                                           Ctrl* ctrl) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!ok) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!(ok = mbar_try_wait(bar, parity))) {
+      if (sh->abort) break;
+      if (globaltimer_ns() - t0 > kTimeoutNs) {
+        sh->abort = 1;
+        atomicOr(&ctrl->status, ST_TIMEOUT);
+        break;
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
+// A: PrefArgs (STREAM_STATS, STREAM_GRAD) or PolicyArgs; W likewise.
+template <class T, int kMode, class A, class W>
+__global__ void __launch_bounds__(kStreamThreads, 2) stream_kernel(A a, W w) {
+  constexpr int kV = Row<T>::kV;
+  extern __shared__ __align__(16) uint8_t ring[];
+  Granule* stages = reinterpret_cast<Granule*>(ring);
+  StreamShared* sh =
+      reinterpret_cast<StreamShared*>(ring + (size_t)kStages * kStageGranules * 16);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&sh->full[i], 1);
+      mbar_init(&sh->empty[i], kWarps);
+    }
+    sh->abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  wait_prior_grid();
+  allow_next_grid();
+  const int64_t rows = a.logits.rows;
+  const T* logits = static_cast<const T*>(a.logits.p);
+  float inv_t = 1.0f;
+  if constexpr (kMode == STREAM_POLICY) inv_t = 1.0f / a.temperature;
+  const float scale = kLog2e * inv_t;
+  const bool write = kMode != STREAM_STATS && a.grad.p;
+  // the i-th row of the block (the gradient's pass goes through the rows backwards)
+  auto row_at = [&](int64_t i) {
+    const int64_t t = blockIdx.x + i * gridDim.x;
+    return kMode == STREAM_GRAD ? rows - 1 - t : t;
+  };
+  const int64_t mine = rows > blockIdx.x ? (rows - 1 - blockIdx.x) / gridDim.x + 1 : 0;
+
+  if (warp == kWarps) {
+    // ---------------------------------------------------------------- producer warp
+    int stage = 0;
+    uint32_t phase = 0, issued = 0, last_par = 0;
+    const uint64_t last_use = l2_evict_first_policy();
+    bool ok = true;
+    for (int64_t i0 = 0; i0 < mine && ok; i0 += 32) {
+      // the scalars of the next 32 rows, one row per lane
+      RowInfo own{-1, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+      if (i0 + lane < mine) {
+        const int64_t t = row_at(i0 + lane);
+        if constexpr (kMode == STREAM_POLICY) {
+          if (load_info(a, t, own)) set_status(w.ctrl, ST_BAD_INDEX);
+        } else {
+          own.target = a.targets.at(t);
+          if (own.target >= a.logits.cols || own.target < 0) {
+            if (kMode == STREAM_STATS && own.target >= 0) set_status(w.ctrl, ST_BAD_INDEX);
+            own.target = -1;
+          }
+          if (kMode == STREAM_GRAD) {  // (maximum, sum, factor)
+            own.old_logp = w.m[t];
+            own.ref_logp = w.s[t];
+            own.weight = w.coef[t];
+            if (own.weight == 0.0f) own.target = -1;
+          }
+        }
+        if (own.target >= 0) own.xt = Elem<T>::get(logits[t * a.logits.ld + own.target]);
+      }
+      for (int i = 0; i < 32 && i0 + i < mine && ok; ++i) {
+        const Row<T> row(logits + row_at(i0 + i) * a.logits.ld, a.logits.cols);
+        // a row that is not read still passes one empty stage, which carries its scalars
+        const bool read = __shfl_sync(0xffffffffu, own.target, i) >= 0;
+        const int n = read && row.whole1 > row.whole0 ? row.whole1 - row.whole0 : 0;
+        const int passes = kMode == STREAM_POLICY && write && n ? 2 : 1;
+        for (int p = 0; p < passes && ok; ++p)
+          for (int g = 0; (g < n || g == 0) && ok; g += kStageGranules) {
+            ok = stage_wait(&sh->empty[stage], phase ^ 1u, sh, w.ctrl);
+            if (!ok) break;
+            if (p == 0 && g == 0 && lane == i) sh->info[stage] = own;
+            __syncwarp();
+            if (lane == 0) {
+              const int m = n - g < kStageGranules ? n - g : kStageGranules;
+              if (m > 0) {
+                mbar_expect_tx(&sh->full[stage], (uint32_t)m * 16);
+                void* dst = stages + stage * kStageGranules;
+                const T* src = row.x + row.first(row.whole0 + g);
+                // read for the last time: the first lines that L2 may drop
+                if (kMode == STREAM_GRAD || p == 1)
+                  bulk_load_hint(dst, src, (uint32_t)m * 16, &sh->full[stage], last_use);
+                else
+                  bulk_load(dst, src, (uint32_t)m * 16, &sh->full[stage]);
+                issued |= 1u << stage;
+                last_par = (last_par & ~(1u << stage)) | (phase << stage);
+              } else {  // (an earlier copy into this stage has landed: it was consumed)
+                mbar_arrive(&sh->full[stage]);
+                issued &= ~(1u << stage);
+              }
+            }
+            if (++stage == kStages) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+      }
+    }
+    if (lane == 0)  // every copy has landed before the block may exit
+      for (int st = 0; st < kStages; ++st)
+        if (issued & (1u << st)) {
+          const uint64_t t0 = globaltimer_ns();
+          while (!mbar_try_wait(&sh->full[st], (last_par >> st) & 1u) &&
+                 globaltimer_ns() - t0 < kTimeoutNs) {
+          }
+        }
+    return;
+  }
+
+  // ------------------------------------------------------------------ the other warps
+  const int tid = threadIdx.x;
+  auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(kBlock) : "memory"); };
+  // whether every warp's waits have succeeded: all of them leave together, so that none is
+  // left at a barrier
+  auto meet_ok = [](bool ok) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"(ok ? 1u : 0u), "n"(kBlock)
+        : "memory");
+    return all != 0;
+  };
+  int stage = 0;
+  uint32_t phase = 0;
+  auto release = [&] {  // this warp has read the stage
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh->empty[stage]);
+    if (++stage == kStages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  };
+  bool ok = true;
+  for (int64_t i = 0; i < mine; ++i) {
+    const int64_t t = row_at(i);
+    const Row<T> row(logits + t * a.logits.ld, a.logits.cols);
+    RowInfo f{-1, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    if (ok) ok = stage_wait(&sh->full[stage], phase, sh, w.ctrl);
+    if (ok) f = sh->info[stage];
+    if (kMode == STREAM_GRAD && !ok) break;  // (no barriers in this mode)
+    const bool read = f.target >= 0;
+    const int n = read && row.whole1 > row.whole0 ? row.whole1 - row.whole0 : 0;
+    // granules shared with other rows: the first (thread 0), the last (thread 32)
+    int edge = -1;
+    if (tid == 0 && row.whole0 > 0) edge = 0;
+    if (tid == 32 && row.whole1 < row.granules && (row.granules > 1 || row.whole0 == 0))
+      edge = row.granules - 1;
+    Granule eg = no_granule<T>();
+    if (read && edge >= 0) eg = row.load(edge);
+
+    MaxSum r{0.0f, 1.0f};
+    RowLoss o{0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    if (kMode != STREAM_GRAD) {
+      if (read) {
+        MaxSum acc{-INFINITY, 0.0f};
+        for (int g = 0; g < n || g == 0; g += kStageGranules) {
+          if (g > 0 && !(ok = stage_wait(&sh->full[stage], phase, sh, w.ctrl))) break;
+          const Granule* buf = stages + stage * kStageGranules + tid;
+          Granule p[kU];
+          if (n - g >= kStageGranules) {
+#pragma unroll
+            for (int u = 0; u < kU; ++u) p[u] = buf[u * kBlock];
+          } else {
+#pragma unroll
+            for (int u = 0; u < kU; ++u)
+              p[u] = g + tid + u * kBlock < n ? buf[u * kBlock] : no_granule<T>();
+          }
+          release();
+          acc = join(acc, granules_max_sum<T, kU>(p, scale));
+        }
+        if (edge >= 0) {
+          const Granule p[1] = {eg};
+          acc = join(acc, granules_max_sum<T, 1>(p, scale));
+        }
+        acc = join_lanes<32>(acc);
+        if (lane == 0) sh->part[warp] = acc;
+      } else if (ok) {
+        release();
+      }
+      if (!meet_ok(ok)) break;
+      if (warp == 0) {
+        if (read) r = join_lanes<kWarps>(sh->part[lane % kWarps]);
+        if constexpr (kMode == STREAM_POLICY) {
+          o = policy_row(a, f, r, inv_t, scale);
+          if (lane == 0) {
+            put_row_loss(a, w, t, o);
+            sh->sum = r;
+            sh->loss = o;
+          }
+        } else if (lane == 0) {
+          put_stats(w, t, read ? r : MaxSum{0.0f, 0.0f},
+                    read ? log_prob(f.xt, r, scale) : 0.0f);
+        }
+      }
+      meet();
+    }
+    if (kMode == STREAM_STATS || !write) continue;
+    float g = f.weight;
+    bool zero = !read;
+    if constexpr (kMode == STREAM_POLICY) {
+      r = sh->sum;
+      o = sh->loss;
+      g = o.g;
+      zero = f.weight == 0.0f || o.none();
+    } else {
+      r = {f.old_logp, f.ref_logp};
+    }
+    T* out = static_cast<T*>(a.grad.p) + t * a.grad.ld;
+    const bool al = same_phase(row.x, out);
+    if (!read) {
+      if (kMode == STREAM_GRAD) release();
+      for (int q = tid; q < row.granules; q += kBlock)
+        put_granule(row, out, al, q, Granule{{0u, 0u, 0u, 0u}});
+      continue;
+    }
+    const float k = -g / r.s;
+    for (int q = 0; q < n || (kMode == STREAM_GRAD && q == 0); q += kStageGranules) {
+      if ((kMode == STREAM_POLICY || q > 0) &&
+          !(ok = stage_wait(&sh->full[stage], phase, sh, w.ctrl)))
+        break;
+      const Granule* buf = stages + stage * kStageGranules + tid;
+      const int first = row.whole0 + q + tid;
+      if (al && n - q >= kStageGranules) {
+        Granule p[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) p[u] = buf[u * kBlock];
+        release();
+        T* dst = out + row.first(first);
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+          store_streamed(dst + u * kBlock * kV, zero ? Granule{{0u, 0u, 0u, 0u}}
+                                                     : softmax_part<T>(p[u], scale, r.m, k));
+      } else {
+#pragma unroll 1
+        for (int u = 0; u < kU; ++u)
+          if (q + tid + u * kBlock < n)
+            put_granule(row, out, al, first + u * kBlock,
+                        zero ? Granule{{0u, 0u, 0u, 0u}}
+                             : softmax_part<T>(buf[u * kBlock], scale, r.m, k));
+        release();
+      }
+    }
+    if (!ok) continue;  // (and leave at the next row, with the other warps)
+    if (edge >= 0)
+      put_granule(row, out, al, edge, zero ? Granule{{0u, 0u, 0u, 0u}}
+                                           : softmax_part<T>(eg, scale, r.m, k));
+    // the thread that stored the target's granule sets the target
+    const int tg = (int)((f.target + row.shift) / kV);
+    const bool whole = row.whole(tg);
+    if (!zero && (whole ? (tg - row.whole0) % kBlock == tid : tg == edge))
+      out[f.target] = Elem<T>::put(target_grad(g, f.xt, r, scale));
+  }
+  if constexpr (kMode == STREAM_POLICY) policy_sums(a, w);
 }
 
 template <class... P, class... A>
@@ -613,39 +880,44 @@ unsigned blocks_for(int64_t items, int64_t most) {
   return (unsigned)(items < 1 ? 1 : items < most ? items : most);
 }
 
-template <class T, int kT>
+template <class T, int kMode, class A, class W>
+cudaError_t launch_stream(const A& a, const W& w, Ctx& c) {
+  const auto fn = stream_kernel<T, kMode, A, W>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kStreamSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3(blocks_for(a.logits.rows, 2 * c.num_sms));
+  cfg.blockDim = dim3(kStreamThreads);
+  cfg.dynamicSmemBytes = kStreamSmem;
+  cfg.stream = c.stream;
+  add_pdl_attr(c, cfg, attr);
+  ++c.launches;
+  return cudaLaunchKernelEx(&cfg, fn, a, w);
+}
+
+template <class T>
 cudaError_t pref_typed(const PrefArgs& p, const PrefWs& w, Ctx& c) {
-  constexpr int kV = 16 / sizeof(T), kItems = kBlock / kT;
   const int64_t rows = p.logits.rows;
+  const bool warps = p.logits.cols <= kWarpCols;
+  const unsigned blocks = (unsigned)((rows + kWarps - 1) / kWarps);
   cudaError_t e = cudaSuccess;
   if (rows)
-    e = launch(c, blocks_for((rows + kItems - 1) / kItems, 1 << 20), kBlock,
-               pref_stats_kernel<T, kT>, p, w);
+    e = warps ? launch(c, blocks, kBlock, pref_stats_warp_kernel<T>, p, w)
+              : launch_stream<T, STREAM_STATS>(p, w, c);
   if (e == cudaSuccess) e = launch(c, (unsigned)p.pairs, kBlock, pref_pair_kernel, p, w);
-  if (e == cudaSuccess && rows && p.grad.p) {
-    // (one granule more than cols / kV for rows that do not start on one)
-    int64_t segs = ((p.logits.cols + kV - 1) / kV + 1 + kT * 4 - 1) / (kT * 4);
-    if (kT == 32) segs = 1;
-    e = launch(c, blocks_for((rows * segs + kItems - 1) / kItems, 1 << 20), kBlock,
-               pref_grad_kernel<T, kT>, p, w, segs);
-  }
+  if (e == cudaSuccess && rows && p.grad.p)
+    e = warps ? launch(c, blocks, kBlock, pref_grad_warp_kernel<T>, p, w)
+              : launch_stream<T, STREAM_GRAD>(p, w, c);
   return e;
-}
-template <class T>
-cudaError_t pref_by_width(const PrefArgs& p, const PrefWs& w, Ctx& c) {
-  return p.logits.cols <= kWarpCols ? pref_typed<T, 32>(p, w, c) : pref_typed<T, kBlock>(p, w, c);
 }
 
 template <class T>
 cudaError_t policy_typed(const PolicyArgs& p, const PolicyWs& w, Ctx& c) {
-  const int64_t rows = p.logits.rows;
-  if (p.logits.cols <= kWarpCols)
-    return launch(c, blocks_for((rows + 7) / 8, 4 * c.num_sms), kBlock,
-                  policy_kernel<T, 32, kBlock>, p, w);
-  if (p.logits.cols <= kBlockCols)
-    return launch(c, blocks_for(rows, 4 * c.num_sms), kBlock, policy_kernel<T, kBlock, kBlock>, p,
-                  w);
-  return launch(c, blocks_for(rows, 2 * c.num_sms), 512, policy_kernel<T, 512, 512>, p, w);
+  if (p.logits.cols > kWarpCols) return launch_stream<T, STREAM_POLICY>(p, w, c);
+  return launch(c, blocks_for((p.logits.rows + kWarps - 1) / kWarps, 3 * c.num_sms), kBlock,
+                policy_warp_kernel<T>, p, w);
 }
 
 }  // namespace
@@ -663,9 +935,9 @@ cudaError_t launch_preference(const PrefArgs& p, void* ws, Ctx& c) {
   auto f = [&](size_t o) { return reinterpret_cast<float*>(b + o); };
   const PrefWs w{reinterpret_cast<Ctrl*>(b), f(L.off_m), f(L.off_s), f(L.off_lp), f(L.off_coef),
                  reinterpret_cast<double*>(b + L.off_loss)};
-  if (p.logits.dtype == CASGD_F32) return pref_by_width<float>(p, w, c);
-  if (p.logits.dtype == CASGD_BF16) return pref_by_width<__nv_bfloat16>(p, w, c);
-  return pref_by_width<__half>(p, w, c);
+  if (p.logits.dtype == CASGD_F32) return pref_typed<float>(p, w, c);
+  if (p.logits.dtype == CASGD_BF16) return pref_typed<__nv_bfloat16>(p, w, c);
+  return pref_typed<__half>(p, w, c);
 }
 
 cudaError_t launch_policy(const PolicyArgs& p, void* ws, Ctx& c) {
