@@ -4,24 +4,35 @@
 //   Y_e = X_e W_e^T      dX_e = dY_e W_e      dW_e = dY_e^T X_e
 //
 // 16-bit inputs, FP32 accumulation in tensor memory, one rounding.  One persistent launch
-// for all groups: every CTA reads the offsets (they live on the device, so no host has to
-// know the groups' sizes), lays the groups' output tiles of 128 x BN out in one list and
-// takes every gridDim-th tile.
+// for all groups: every CTA pair reads the offsets (they live on the device, so no host has
+// to know the groups' sizes), lays the groups' output tiles out in one list and takes every
+// pair-count-th tile.
+//
+// Tiles.  A pair of CTAs computes 256 x N accumulators (tcgen05.mma.cta_group::2), whose
+// M side is a dimension of the weights and whose N side, any multiple of 32 up to 256, is
+//   Y, dX   the tokens: accumulators are transposed (Y^T = W X^T), so that a group's ragged
+//           length meets the side whose size an instruction can choose; a group's tokens
+//           are cut into equal tiles.  32 tokens cost 32 / 256 of a full tile's products.
+//   dW      the other dimension of the weights; the tokens are summed over.
+// Each CTA stages its 128 rows of the M side and its half of the N side, 64 deep: 32 KB for
+// 256 x 256 x 64 products, two thirds of what one CTA needs for a 128 x 256 tile of its own
+// (reads from L2 bound that form: it reached half of the tensor peak).
 //
 //   warp 0     TMA producer: 64-deep slices of both operands into a ring of stages;
-//   warp 1     issues tcgen05.mma (128 x BN x 16) into one of two TMEM accumulators, so
-//              that a tile's epilogue overlaps the next tile's products;
-//   warps 2-5  epilogue: TMEM -> registers -> one rounding -> shared memory (to turn rows
-//              per lane into 128-byte row segments) -> masked stores.
+//   warp 1     (leader) issues the MMAs into one of two TMEM accumulators, so that a
+//              tile's epilogue overlaps the next tile's products;
+//   warps 2-5  epilogue: TMEM -> registers -> one rounding -> shared memory (to turn them
+//              into row segments) -> masked stores;
+//   warp 6     (dW) the ragged end of the summed tokens.
 //
-// Tiles at a group's ragged end.  In Y and dX the rows are the tile's M side: rows past
-// the end are other groups' and are computed and dropped (a row of the accumulator depends
-// on its own row of A alone).  In dW they are the summed side: only whole steps of 16 rows
-// are issued, and the rows past the end in the last step are set to zero in both operands
-// in shared memory first, since zero times another group's infinity would not be zero.
+// Ragged ends.  In Y and dX rows past a group's end are computed and dropped (a column of
+// the accumulator depends on its own token alone).  In dW only whole steps of 16 tokens are
+// issued, and the tokens past the end in the last step, which are other groups', are set to
+// zero in both operands in shared memory first, since zero times another group's infinity
+// would not be zero.
 // The operand layouts: k runs along the 128-byte rows of both operands in Y; in dX the
-// weights are summed over their rows (n), in dW both operands are summed over their rows,
-// which the MMA takes as MN-major operands, so nothing is transposed in memory.
+// weights are summed over their rows (n), in dW both operands over theirs, which the MMA
+// takes as MN-major operands, so nothing is transposed in memory.
 //
 // TMA needs rows on 16-byte boundaries.  Inputs without them (odd widths or pitches) are
 // copied once into the workspace with padded rows; outputs without them are stored element
@@ -37,34 +48,33 @@ namespace {
 constexpr size_t kAlign = 256;
 inline size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
-constexpr int BM = 128, BK = 64;
-constexpr int kThreads = 192;
-constexpr int kABytes = BM * BK * 2;
+constexpr int BM = 256, BN = 256, BK = 64;  // tile of a pair
+constexpr int kHalf = 128 * BK * 2;         // a CTA's 128 rows of a slice of one operand
+constexpr int kStageBytes = 2 * kHalf;
+constexpr int kStages = 6;
 constexpr int kMaxGroups = CASGD_MAX_GROUPS;
 constexpr uint64_t kTimeoutNs = 1000000000ull;
-constexpr int kOutBytes = 4 * 32 * 128;  // per epilogue warp: 32 rows of 64 16-bit values
-
-template <int BN>
-struct Ring {
-  static constexpr int kBBytes = BN * BK * 2;
-  static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 6 : 8;
-  static constexpr uint32_t kTmemCols = 2 * BN;
-};
+constexpr int kOutBytes = 4 * 32 * 128;  // per epilogue warp: 4 KB
+constexpr uint32_t kTmemCols = 2 * BN;
+template <int kDir>
+constexpr int kThreads = kDir == GROUP_DW ? 224 : 192;
 
 struct Shared {
-  uint64_t full[8], empty[8], tfull[2], tempty[2], drain;
+  uint64_t full[kStages];   // leader: both CTAs' copies of a stage are in
+  uint64_t empty[kStages];  // both: the MMAs have read a stage
+  uint64_t tail[kStages];   // dW, both: this CTA's copies of a ragged slice are in
+  uint64_t mend[kStages];   // dW, leader: the other CTA's are in and mended
+  uint64_t tfull[2];        // both: an accumulator is complete
+  uint64_t tempty[2];       // leader: both CTAs' epilogues are done with it (8 warps)
+  uint64_t drain;
   uint32_t tmem_base;
   volatile uint32_t abort;
   int32_t tiles;
   int32_t row0[kMaxGroups + 2];   // first row of each group, held ascending
   int32_t tile0[kMaxGroups + 2];  // first tile of each group
 };
-
-template <int BN>
-constexpr size_t smem_bytes() {
-  return (size_t)Ring<BN>::kStages * Ring<BN>::kStageBytes + kOutBytes + sizeof(Shared) + 1024;
-}
+constexpr size_t kSmemBytes = (size_t)kStages * kStageBytes + kOutBytes + sizeof(Shared) + 1024;
+static_assert(kSmemBytes <= 232448, "dynamic shared memory per CTA");
 
 struct GroupTc {
   const int32_t* offsets;
@@ -77,11 +87,12 @@ struct GroupTc {
 
 // Bounded wait: false (and the CTA's abort word set) if the phase does not complete in
 // time or another role of this CTA gave up.
+template <bool kCluster = false>  // acquiring what the other CTA released
 __device__ bool wait_on(uint64_t* bar, uint32_t parity, Shared* sh, Ctrl* ctrl) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (kCluster ? tile::try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   while (true) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (kCluster ? tile::try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
     if (sh->abort) return false;
     if (globaltimer_ns() - t0 > kTimeoutNs) {
       sh->abort = 1;
@@ -93,18 +104,17 @@ __device__ bool wait_on(uint64_t* bar, uint32_t parity, Shared* sh, Ctrl* ctrl) 
 
 // Groups' first rows (each at least the one before, inside [0, rows]) and first tiles.
 // Y and dX have one more group: the rows after the last offset, which receive zeros.
-template <int kDir, int BN>
+template <int kDir>
 __device__ void lay_out_tiles(const GroupTc& a, Shared* sh) {
   const int E = a.groups;
-  for (int e = threadIdx.x; e <= E; e += kThreads) sh->row0[e] = a.offsets[e];
+  for (int e = threadIdx.x; e <= E; e += kThreads<kDir>) sh->row0[e] = a.offsets[e];
   __syncthreads();
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
-    const int nt = ((kDir == GROUP_Y ? a.n : a.k) + BN - 1) / BN;
-    const int per_dw = (a.n + BM - 1) / BM * nt;
+    const int mt = ((kDir == GROUP_DX ? a.k : a.n) + BM - 1) / BM;
+    const int per_dw = mt * ((a.k + BN - 1) / BN);
     int top = 0, tiles = 0;
     bool bad = false;
-    // row0 for e = 0 .. E, then (below) row0[E+1] = rows
     for (int e0 = 0; e0 <= E; e0 += 32) {
       const int e = e0 + lane;
       const int raw = e <= E ? sh->row0[e] : 0;
@@ -128,7 +138,7 @@ __device__ void lay_out_tiles(const GroupTc& a, Shared* sh) {
       const int e = e0 + lane;
       int t = 0;
       if (e < last)
-        t = kDir == GROUP_DW ? per_dw : (sh->row0[e + 1] - sh->row0[e] + BM - 1) / BM * nt;
+        t = kDir == GROUP_DW ? per_dw : (sh->row0[e + 1] - sh->row0[e] + BN - 1) / BN * mt;
       int inc = t;
 #pragma unroll
       for (int o = 1; o < 32; o *= 2) {
@@ -148,12 +158,13 @@ __device__ void lay_out_tiles(const GroupTc& a, Shared* sh) {
 }
 
 struct Tile {
-  int e, m0, n0;   // group, first row / column of the tile (dW: of W_e)
-  int row0, rows;  // the group's rows
-  int nkb;         // 64-deep slices to sum (0: the tile is zeros)
+  int e, row0, rows;  // group and its rows
+  int m0;             // first index of the weights' dimension on the M side
+  int n0, n, valid;   // N side: first token of the group (dW: first k), MMA size, real size
+  int depth, nkb;     // summed length and its 64-deep slices (0: the tile is zeros)
 };
 
-template <int kDir, int BN>
+template <int kDir>
 __device__ __forceinline__ Tile tile_at(const GroupTc& a, const Shared* sh, int t) {
   int lo = 0, hi = kDir == GROUP_DW ? a.groups : a.groups + 1;  // the last e with tile0 <= t
   while (hi - lo > 1) {
@@ -165,11 +176,15 @@ __device__ __forceinline__ Tile tile_at(const GroupTc& a, const Shared* sh, int 
   r.row0 = sh->row0[lo];
   r.rows = sh->row0[lo + 1] - r.row0;
   const int local = t - sh->tile0[lo];
-  const int mt = ((kDir == GROUP_DW ? a.n : r.rows) + BM - 1) / BM;
-  r.n0 = local / mt * BN;
-  r.m0 = local % mt * BM;
-  const int depth = kDir == GROUP_Y ? a.k : kDir == GROUP_DX ? a.n : r.rows;
-  r.nkb = kDir != GROUP_DW && lo == a.groups ? 0 : (depth + BK - 1) / BK;
+  const int len = kDir == GROUP_DW ? a.k : r.rows;  // N side
+  const int nt = (len + BN - 1) / BN;               // equal tiles, multiples of 32
+  const int step = ((len + nt - 1) / nt + 31) & ~31;
+  r.m0 = local / nt * BM;
+  r.n0 = local % nt * step;
+  r.valid = len - r.n0 < step ? len - r.n0 : step;
+  r.n = (r.valid + 31) & ~31;
+  r.depth = kDir == GROUP_Y ? a.k : kDir == GROUP_DX ? a.n : r.rows;
+  r.nkb = kDir != GROUP_DW && lo == a.groups ? 0 : (r.depth + BK - 1) / BK;
   return r;
 }
 
@@ -186,14 +201,25 @@ __device__ __forceinline__ uint32_t pack2<__half>(uint32_t lo, uint32_t hi) {
   return reinterpret_cast<const uint32_t&>(v);
 }
 
-// One warp's 32 rows of a tile: 64 columns at a time, one row per lane into a staging
-// buffer (16-byte chunk c of row r at slot c ^ (r % 8), so neither side has bank
-// conflicts), then four rows of 128 bytes per store instruction.
-template <class T, int BN>
-__device__ __forceinline__ void store_tile(const GroupTc& a, uint16_t* out, int rows, int cols,
+// Eight 16-bit values, the first `count` of them, to dst.
+__device__ __forceinline__ void store8(uint16_t* dst, uint4 v, int count, bool vec) {
+  if (vec && count >= 8) {
+    *reinterpret_cast<uint4*>(dst) = v;
+    return;
+  }
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < count) dst[j] = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
+}
+
+// dW: one warp's 32 rows (n) of a tile, `rows` x `cols` of them real.  64 columns at a
+// time, one row per lane into a staging buffer (16-byte chunk c of row r at slot
+// c ^ (r % 8), so neither side has bank conflicts), then four rows of 128 bytes per store.
+template <class T>
+__device__ __forceinline__ void store_rows(const GroupTc& a, uint16_t* out, int rows, int cols,
                                            uint32_t taddr, bool zero, uint8_t* stage, int lane) {
-  for (int c0 = 0; c0 < BN; c0 += 64) {
-    if (c0 >= cols) break;
+  for (int c0 = 0; c0 < cols; c0 += 64) {
     uint32_t lo[32], hi[32];
     if (!zero) {
       __syncwarp();
@@ -221,103 +247,150 @@ __device__ __forceinline__ void store_tile(const GroupTc& a, uint16_t* out, int 
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int r = 4 * i + (lane >> 3);
-      if (r >= rows || col >= cols) continue;
-      const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((c ^ (r & 7)) * 16));
-      uint16_t* dst = out + (int64_t)r * a.ldo + col;
-      if (a.vec_out && col + 8 <= cols) {
-        *reinterpret_cast<uint4*>(dst) = v;
-      } else {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        for (int j = 0; j < 8 && col + j < cols; ++j)
-          dst[j] = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
-      }
+      if (r < rows && col < cols)
+        store8(out + (int64_t)r * a.ldo + col,
+               *reinterpret_cast<const uint4*>(stage + r * 128 + ((c ^ (r & 7)) * 16)),
+               cols - col, a.vec_out);
     }
   }
 }
 
-// mapA: X (Y), dY (dX, dW); mapA16: the same in boxes of 16 rows (Y, dX); mapB: W (Y, dX),
-// X (dW).
-template <class T, int kDir, int BN>
-__global__ void __launch_bounds__(kThreads, 1)
-    group_kernel(const __grid_constant__ CUtensorMap mapA,
-                 const __grid_constant__ CUtensorMap mapA16,
-                 const __grid_constant__ CUtensorMap mapB, const GroupTc a) {
-  using R = Ring<BN>;
+// Y, dX: one warp's 32 columns of the output (TMEM lanes) for `tokens` tokens (TMEM
+// columns), `cols` of them real.  32 tokens at a time, a lane's column of each into the
+// staging buffer, then eight tokens' 64-byte segments per store.
+template <class T>
+__device__ __forceinline__ void store_tokens(const GroupTc& a, uint16_t* out, int tokens, int cols,
+                                             uint32_t taddr, bool zero, uint8_t* stage, int lane) {
+  uint16_t* st = reinterpret_cast<uint16_t*>(stage);
+  for (int t0 = 0; t0 < tokens; t0 += 32) {
+    uint32_t v[32];
+    if (!zero) {
+      __syncwarp();
+      tile::tmem_load32(taddr + t0, v);
+      tile::tmem_wait(v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) v[e] = 0u;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      const uint32_t p = pack2<T>(v[e], v[e + 1]);
+      st[e * 32 + lane] = (uint16_t)p;
+      st[(e + 1) * 32 + lane] = (uint16_t)(p >> 16);
+    }
+    __syncwarp();
+    const int col = (lane & 3) * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = 8 * i + (lane >> 2);
+      if (t0 + t < tokens && col < cols)
+        store8(out + (int64_t)(t0 + t) * a.ldo + col,
+               *reinterpret_cast<const uint4*>(st + t * 32 + col), cols - col, a.vec_out);
+    }
+  }
+}
+
+// mapM, mapN: the operand on the M and on the N side (Y: W, X; dX: W, dY; dW: dY, X);
+// mapN16: the N side's in boxes of 16 rows (Y, dX).
+template <class T, int kDir>
+__global__ void __launch_bounds__(kThreads<kDir>, 1)
+    group_kernel(const __grid_constant__ CUtensorMap mapM, const __grid_constant__ CUtensorMap mapN,
+                 const __grid_constant__ CUtensorMap mapN16, const GroupTc a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~(uintptr_t)1023);
-  uint8_t* out_stage = smem + (size_t)R::kStages * R::kStageBytes;
+  uint8_t* out_stage = smem + (size_t)kStages * kStageBytes;
   Shared* sh = reinterpret_cast<Shared*>(out_stage + kOutBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)tile::cluster_rank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < R::kStages; ++i) {
+    for (int i = 0; i < kStages; ++i) {
       mbar_init(&sh->full[i], 1);
       mbar_init(&sh->empty[i], 1);
+      mbar_init(&sh->tail[i], 1);
+      mbar_init(&sh->mend[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh->tfull[i], 1);
-      mbar_init(&sh->tempty[i], 4);
+      mbar_init(&sh->tempty[i], 8);
     }
     mbar_init(&sh->drain, 1);
     sh->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 1) tile::tmem_alloc(&sh->tmem_base, R::kTmemCols);
+  if (warp == 1) tile::tmem_alloc(&sh->tmem_base, kTmemCols);
   wait_prior_grid();
   allow_next_grid();
   tile::fence_before();
-  lay_out_tiles<kDir, BN>(a, sh);  // (synchronises the block)
+  lay_out_tiles<kDir>(a, sh);  // (synchronises the CTA)
+  tile::cluster_sync();
   tile::fence_after();
   const uint32_t tmem = sh->tmem_base;
   const int tiles = sh->tiles;
+  // dW: whether slice kb of a tile ends inside a step of 16
+  auto ragged = [](const Tile& c, int kb) {
+    return kDir == GROUP_DW && kb == c.nkb - 1 && (c.depth & 15) != 0;
+  };
 
   if (warp == 0) {
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0, issued = 0, last_par = 0;
       bool ok = true;
-      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-        const Tile c = tile_at<kDir, BN>(a, sh, t);
-        const int valid = c.rows - c.m0;
-        // few rows (decoding): only the 16-row boxes that hold some
-        const int boxes16 = kDir != GROUP_DW && valid <= 64 ? (valid + 15) / 16 : 0;
+      for (int t = pair; t < tiles && ok; t += pairs) {
+        const Tile c = tile_at<kDir>(a, sh, t);
+        const int half = c.n / 2;  // this CTA's part of the N side
+        const int boxes64 = (half + 63) / 64;
+        const uint32_t bytes =
+            kHalf + (kDir == GROUP_DW ? (uint32_t)boxes64 * 8192 : (uint32_t)half * 128);
+        const int m = c.m0 + rank * 128;
         for (int kb = 0; kb < c.nkb; ++kb) {
           if (!wait_on(&sh->empty[stage], phase ^ 1u, sh, a.ctrl)) {
             ok = false;
             break;
           }
-          const uint32_t sa = smem_u32(smem + (size_t)stage * R::kStageBytes);
-          const uint32_t sb = sa + kABytes;
-          uint64_t* bar = &sh->full[stage];
-          mbar_expect_tx(bar, (boxes16 ? boxes16 * 2048 : kABytes) + R::kBBytes);
+          const uint32_t sm = smem_u32(smem + (size_t)stage * kStageBytes), sn = sm + kHalf;
+          const uint32_t lead = tile::peer_addr(&sh->full[stage], 0);
+          uint32_t bar = lead;
+          if (ragged(c, kb)) {
+            bar = tile::peer_addr(&sh->tail[stage], rank);
+            mbar_expect_tx(&sh->tail[stage], bytes);
+          } else if (leader) {
+            mbar_expect_tx(&sh->full[stage], 2 * bytes);
+          }
           const int d = kb * BK;
           if (kDir == GROUP_DW) {
-            for (int i = 0; i < BM / 64; ++i)
-              tile::tma_load_2d(sa + i * 8192, &mapA, bar, c.m0 + i * 64, c.row0 + d);
-            for (int i = 0; i < BN / 64; ++i)
-              tile::tma_load_2d(sb + i * 8192, &mapB, bar, c.n0 + i * 64, c.row0 + d);
+            for (int i = 0; i < 2; ++i)
+              tile::tma_load_2d(sm + i * 8192, &mapM, bar, m + i * 64, c.row0 + d);
+            for (int i = 0; i < boxes64; ++i)
+              tile::tma_load_2d(sn + i * 8192, &mapN, bar, c.n0 + rank * half + i * 64,
+                                c.row0 + d);
           } else {
-            if (boxes16)
-              for (int i = 0; i < boxes16; ++i)
-                tile::tma_load_2d(sa + i * 2048, &mapA16, bar, d, c.row0 + c.m0 + i * 16);
-            else
-              tile::tma_load_2d(sa, &mapA, bar, d, c.row0 + c.m0);
             if (kDir == GROUP_Y)
-              tile::tma_load_3d(sb, &mapB, bar, d, c.n0, c.e);
+              tile::tma_load_3d(sm, &mapM, bar, d, m, c.e);
             else
-              for (int i = 0; i < BN / 64; ++i)
-                tile::tma_load_3d(sb + i * 8192, &mapB, bar, c.n0 + i * 64, d, c.e);
+              for (int i = 0; i < 2; ++i)
+                tile::tma_load_3d(sm + i * 8192, &mapM, bar, m + i * 64, d, c.e);
+            const int row = c.row0 + c.n0 + rank * half;
+            if (half == 128)
+              tile::tma_load_2d(sn, &mapN, bar, d, row);
+            else
+              for (int i = 0; i < half / 16; ++i)
+                tile::tma_load_2d(sn + i * 2048, &mapN16, bar, d, row + i * 16);
           }
           issued |= 1u << stage;
           last_par = (last_par & ~(1u << stage)) | (phase << stage);
-          if (++stage == R::kStages) {
+          if (++stage == kStages) {
             stage = 0;
             phase ^= 1u;
           }
         }
       }
-      // every copy has landed before the CTA may exit
-      for (int st = 0; st < R::kStages; ++st)
+      // every copy of the pair has landed before the CTAs may exit
+      for (int st = 0; st < kStages && leader; ++st)
         if (issued & (1u << st)) {
           const uint64_t t0 = globaltimer_ns();
           while (!mbar_try_wait(&sh->full[st], (last_par >> st) & 1u) &&
@@ -326,84 +399,57 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
   } else if (warp == 1) {
-    constexpr bool kBf16 = sizeof(T) == 2 && !__is_same(T, __half);
-    constexpr uint32_t kIdesc =
-        tile::instr_desc(BM, BN, kBf16, kDir == GROUP_DW, kDir != GROUP_Y);
-    constexpr uint32_t kAStep = kDir == GROUP_DW ? 128 : 2;   // 16 of the depth, >> 4
-    constexpr uint32_t kBStep = kDir == GROUP_Y ? 2 : 128;
-    int stage = 0, iter = 0;
-    uint32_t phase = 0, tphase[2] = {0, 0};
-    bool ok = true, any = false;
-    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-      const Tile c = tile_at<kDir, BN>(a, sh, t);
-      if (c.nkb == 0) continue;
-      const int acc = iter++ & 1;
-      ok = __shfl_sync(0xffffffffu,
-                       lane == 0 ? (int)wait_on(&sh->tempty[acc], tphase[acc] ^ 1u, sh, a.ctrl)
-                                 : 0, 0) != 0;
-      if (!ok) break;
-      tphase[acc] ^= 1u;
-      tile::fence_after();
-      const int depth = kDir == GROUP_Y ? a.k : kDir == GROUP_DX ? a.n : c.rows;
-      for (int kb = 0; kb < c.nkb; ++kb) {
-        ok = __shfl_sync(0xffffffffu,
-                         lane == 0 ? (int)wait_on(&sh->full[stage], phase, sh, a.ctrl) : 0,
-                         0) != 0;
-        if (!ok) break;
-        const int left = depth - kb * BK;
-        const int steps = left >= BK ? BK / 16 : (left + 15) / 16;
-        uint8_t* sp = smem + (size_t)stage * R::kStageBytes;
-        if (kDir == GROUP_DW && left < BK && (left & 15)) {
-          // rows left .. of the last step are other groups': zero in every 64-column block
-          __syncwarp();
-          const int zr = steps * 16 - left;
-          for (int i = lane; i < zr * 8 * (BM + BN) / 64; i += 32) {
-            const int blk = i / (zr * 8), r = i / 8 % zr, ch = i & 7;
-            *reinterpret_cast<uint4*>(sp + blk * 8192 + (left + r) * 128 + ch * 16) =
-                make_uint4(0, 0, 0, 0);
-          }
-          tile::fence_async_smem();
-          __syncwarp();
-        }
-        if (lane == 0) {
+    if (lane == 0 && leader) {
+      constexpr bool kBf16 = !__is_same(T, __half);
+      constexpr uint32_t kMStep = kDir == GROUP_Y ? 2 : 128;  // 16 of the depth, >> 4
+      constexpr uint32_t kNStep = kDir == GROUP_DW ? 128 : 2;
+      int stage = 0, iter = 0;
+      uint32_t phase = 0, tphase[2] = {0, 0};
+      bool ok = true, any = false;
+      for (int t = pair; t < tiles && ok; t += pairs) {
+        const Tile c = tile_at<kDir>(a, sh, t);
+        if (c.nkb == 0) continue;
+        const uint32_t idesc =
+            tile::instr_desc(BM, c.n, kBf16, kDir != GROUP_Y, kDir == GROUP_DW);
+        const int acc = iter++ & 1;
+        if (!(ok = wait_on(&sh->tempty[acc], tphase[acc] ^ 1u, sh, a.ctrl))) break;
+        tphase[acc] ^= 1u;
+        tile::fence_after();
+        for (int kb = 0; kb < c.nkb; ++kb) {
+          if (!(ok = wait_on(&sh->full[stage], phase, sh, a.ctrl))) break;
           tile::fence_after();
-          const uint32_t sa = smem_u32(sp), sb = sa + kABytes;
-          const uint64_t ad = tile::smem_desc(sa, kDir == GROUP_DW ? 8192 : 16, 1024);
-          const uint64_t bd = tile::smem_desc(sb, kDir == GROUP_Y ? 16 : 8192, 1024);
+          const int left = c.depth - kb * BK;
+          const int steps = left >= BK ? BK / 16 : (left + 15) / 16;
+          const uint32_t sm = smem_u32(smem + (size_t)stage * kStageBytes);
+          const uint64_t md = tile::smem_desc(sm, kDir == GROUP_Y ? 16 : 8192, 1024);
+          const uint64_t nd = tile::smem_desc(sm + kHalf, kDir == GROUP_DW ? 8192 : 16, 1024);
           for (int s = 0; s < steps; ++s)
-            tile::mma_16bit(tmem + (uint32_t)(acc * BN), ad + (uint64_t)(s * kAStep),
-                            bd + (uint64_t)(s * kBStep), kIdesc, (kb | s) ? 1u : 0u);
-          tile::mma_commit(&sh->empty[stage]);
+            tile::mma_pair(tmem + (uint32_t)(acc * BN), md + (uint64_t)(s * kMStep),
+                           nd + (uint64_t)(s * kNStep), idesc, (kb | s) ? 1u : 0u);
+          any = true;
+          tile::commit_pair(&sh->empty[stage], 0x3);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
-        any = true;
-        if (++stage == R::kStages) {
-          stage = 0;
-          phase ^= 1u;
+        if (!ok) break;
+        tile::commit_pair(&sh->tfull[acc], 0x3);
+      }
+      if (any) {  // every MMA has completed before the pair frees TMEM
+        tile::commit_pair(&sh->drain, 0x1);
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(&sh->drain, 0) && globaltimer_ns() - t0 < kTimeoutNs) {
         }
       }
-      if (!ok) break;
-      if (lane == 0) tile::mma_commit(&sh->tfull[acc]);
     }
-    if (any && lane == 0) {  // every MMA has completed before TMEM is freed
-      tile::mma_commit(&sh->drain);
-      const uint64_t t0 = globaltimer_ns();
-      while (!mbar_try_wait(&sh->drain, 0) && globaltimer_ns() - t0 < kTimeoutNs) {
-      }
-    }
-    __syncwarp();
-  } else {
+  } else if (warp < 6) {
     const int quarter = warp & 3;  // TMEM lanes 32 * quarter .. + 31
     uint8_t* stage = out_stage + (warp - 2) * (32 * 128);
     int iter = 0;
     uint32_t tphase[2] = {0, 0};
-    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-      const Tile c = tile_at<kDir, BN>(a, sh, t);
-      const int m_end = kDir == GROUP_DW ? a.n : c.rows;
-      const int cols = (kDir == GROUP_Y ? a.n : a.k) - c.n0;
-      const int rows = m_end - c.m0 - quarter * 32;
-      uint16_t* out = a.out + (kDir == GROUP_DW
-                                   ? c.e * a.stride_o + (int64_t)(c.m0 + quarter * 32) * a.ldo
-                                   : (int64_t)(c.row0 + c.m0 + quarter * 32) * a.ldo) + c.n0;
+    for (int t = pair; t < tiles; t += pairs) {
+      const Tile c = tile_at<kDir>(a, sh, t);
       int acc = 0;
       if (c.nkb > 0) {
         acc = iter++ & 1;
@@ -413,21 +459,60 @@ __global__ void __launch_bounds__(kThreads, 1)
         tphase[acc] ^= 1u;
         tile::fence_after();
       }
-      if (rows > 0)
-        store_tile<T, BN>(a, out, rows, cols,
-                          tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * BN),
+      const int m = c.m0 + rank * 128 + quarter * 32;  // this warp's first M index
+      const int m_left = (kDir == GROUP_DX ? a.k : a.n) - m;
+      const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * BN);
+      if (m_left > 0) {
+        if (kDir == GROUP_DW)
+          store_rows<T>(a, a.out + c.e * a.stride_o + (int64_t)m * a.ldo + c.n0, m_left, c.valid,
+                        taddr, c.nkb == 0, stage, lane);
+        else
+          store_tokens<T>(a, a.out + (int64_t)(c.row0 + c.n0) * a.ldo + m, c.valid, m_left, taddr,
                           c.nkb == 0, stage, lane);
+      }
       if (c.nkb > 0) {
         tile::fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->tempty[acc]);
+        if (lane == 0) tile::arrive_cluster(tile::peer_addr(&sh->tempty[acc], 0));
       }
+    }
+  } else if (kDir == GROUP_DW) {
+    // The ragged slices: once this CTA's copies are in, zeros to the tokens past the
+    // group's end in the last step, in every 64-column block of both operands.
+    int stage = 0;
+    uint32_t tails = 0, mends = 0;  // parity of the next use of each stage's barriers
+    for (int t = pair; t < tiles; t += pairs) {
+      const Tile c = tile_at<kDir>(a, sh, t);
+      if (c.nkb > 0 && ragged(c, c.nkb - 1)) {
+        const int st = (stage + c.nkb - 1) % kStages;
+        int ok = 1;
+        if (lane == 0) ok = wait_on(&sh->tail[st], (tails >> st) & 1u, sh, a.ctrl) ? 1 : 0;
+        if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+        tails ^= 1u << st;
+        const int left = c.depth - (c.nkb - 1) * BK, zr = 16 - (left & 15);
+        const int blocks = 2 + (c.n / 2 + 63) / 64;
+        uint8_t* sp = smem + (size_t)st * kStageBytes;
+        for (int i = lane; i < blocks * zr * 8; i += 32)
+          *reinterpret_cast<uint4*>(sp + i / (zr * 8) * 8192 + (left + i / 8 % zr) * 128 +
+                                    (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+        tile::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {  // the leader's warp passes on that both CTAs' are mended
+          if (!leader)
+            tile::arrive_cluster(tile::peer_addr(&sh->mend[st], 0));
+          else if (wait_on<true>(&sh->mend[st], mends >> st & 1u, sh, a.ctrl))
+            mbar_arrive(&sh->full[st]);
+        }
+        mends ^= 1u << st;
+      }
+      stage = (stage + c.nkb) % kStages;
     }
   }
   tile::fence_before();
   __syncthreads();
+  tile::cluster_sync();  // the leader's MMAs and every copy into either CTA are finished
   tile::fence_after();
-  if (warp == 1) tile::tmem_free(tmem, R::kTmemCols);
+  if (warp == 1) tile::tmem_free(tmem, kTmemCols);
 }
 
 // dst (rows x cols8, cols padded to a multiple of 8 with zeros) = src; `parts` matrices.
@@ -528,21 +613,24 @@ Operand weights_of(const GroupArgs& g) {
   return {g.w, g.n, g.k, g.ldw, g.groups, g.stride_w};
 }
 
-template <class T, int kDir, int BN>
-cudaError_t launch_tiles(const GroupArgs& g, Operand A, Operand B, void* ws, Ctx& c) {
+template <class T, int kDir>
+cudaError_t group_typed(const GroupArgs& g, void* ws, Ctx& c) {
   constexpr bool kBf16 = !__is_same(T, __half);
+  Operand M = kDir == GROUP_DW ? rows_of(g.y, g.rows, g.n, g.ldy) : weights_of(g);
+  Operand N = kDir == GROUP_DX ? rows_of(g.y, g.rows, g.n, g.ldy)
+                               : rows_of(g.x, g.rows, g.k, g.ldx);
   char* at = static_cast<char*>(ws) + align_up(sizeof(Ctrl));
   cudaError_t e = cudaSuccess;
-  CUtensorMap ma, ma16, mb;
-  memset(&ma, 0, sizeof(ma));
-  memset(&ma16, 0, sizeof(ma16));
-  memset(&mb, 0, sizeof(mb));
+  CUtensorMap mm, mn, mn16;
+  memset(&mm, 0, sizeof(mm));
+  memset(&mn, 0, sizeof(mn));
+  memset(&mn16, 0, sizeof(mn16));
   if (g.rows > 0) {  // (without rows only zeros are stored: no map is used)
-    if ((e = pad(A, at, c)) != cudaSuccess || (e = pad(B, at, c)) != cudaSuccess) return e;
+    if ((e = pad(M, at, c)) != cudaSuccess || (e = pad(N, at, c)) != cudaSuccess) return e;
     const bool ok = kDir == GROUP_DW
-                        ? encode(&ma, A, 64, BK, kBf16) && encode(&mb, B, 64, BK, kBf16)
-                        : encode(&ma, A, BK, BM, kBf16) && encode(&ma16, A, BK, 16, kBf16) &&
-                              encode(&mb, B, 64, kDir == GROUP_Y ? BN : BK, kBf16);
+                        ? encode(&mm, M, 64, BK, kBf16) && encode(&mn, N, 64, BK, kBf16)
+                        : encode(&mm, M, 64, kDir == GROUP_Y ? 128 : BK, kBf16) &&
+                              encode(&mn, N, BK, 128, kBf16) && encode(&mn16, N, BK, 16, kBf16);
     if (!ok) return cudaErrorInvalidValue;
   }
   GroupTc a;
@@ -557,30 +645,29 @@ cudaError_t launch_tiles(const GroupArgs& g, Operand A, Operand B, void* ws, Ctx
   a.vec_out = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.ldo % 8 == 0 &&
               a.stride_o % 8 == 0;
   a.ctrl = static_cast<Ctrl*>(ws);
-  const int64_t nt = ((kDir == GROUP_Y ? g.n : g.k) + BN - 1) / BN;
-  const int64_t most = kDir == GROUP_DW ? g.groups * ((g.n + BM - 1) / BM) * nt
-                                        : (g.rows / BM + (g.rows < g.groups ? g.rows : g.groups)
-                                           + 1) * nt;
-  const auto fn = group_kernel<T, kDir, BN>;
-  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<BN>());
+  // at most this many tiles, whatever the offsets say
+  const int64_t mt = ((kDir == GROUP_DX ? g.k : g.n) + BM - 1) / BM;
+  const int64_t some = g.rows < g.groups ? g.rows : g.groups;
+  const int64_t most = kDir == GROUP_DW ? g.groups * mt * ((g.k + BN - 1) / BN)
+                                        : (g.rows / BN + some + 1) * mt;
+  const auto fn = group_kernel<T, kDir>;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
   if (e != cudaSuccess) return e;
+  const int64_t pairs = c.num_sms / 2;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  cfg.gridDim = dim3((unsigned)(most < c.num_sms ? most : c.num_sms));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem_bytes<BN>();
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)(2 * (most < pairs ? most : pairs)));
+  cfg.blockDim = dim3(kThreads<kDir>);
+  cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = c.stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   add_pdl_attr(c, cfg, attr);
   ++c.launches;
-  return cudaLaunchKernelEx(&cfg, fn, ma, ma16, mb, a);
-}
-
-template <class T, int kDir>
-cudaError_t group_typed(const GroupArgs& g, void* ws, Ctx& c) {
-  const Operand A = kDir == GROUP_Y ? rows_of(g.x, g.rows, g.k, g.ldx)
-                                    : rows_of(g.y, g.rows, g.n, g.ldy);
-  const Operand B = kDir == GROUP_DW ? rows_of(g.x, g.rows, g.k, g.ldx) : weights_of(g);
-  return launch_tiles<T, kDir, 256>(g, A, B, ws, c);
+  return cudaLaunchKernelEx(&cfg, fn, mm, mn, mn16, a);
 }
 
 template <class T>
