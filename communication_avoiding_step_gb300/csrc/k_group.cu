@@ -82,22 +82,34 @@ struct GroupTc {
   uint16_t* out;
   int64_t ldo, stride_o;
   bool vec_out;  // output rows on 16-byte boundaries
+  // MN-major operands whose width is a multiple of 64 are seen as blocks of 64 columns, one
+  // copy for two blocks (fewer copies: 4 -> 2 per slice in dW, 3 -> 2 in dX)
+  bool blocks_m, blocks_n;
   Ctrl* ctrl;
 };
 
 // Bounded wait: false (and the CTA's abort word set) if the phase does not complete in
-// time or another role of this CTA gave up.
-template <bool kCluster = false>  // acquiring what the other CTA released
-__device__ bool wait_on(uint64_t* bar, uint32_t parity, Shared* sh, Ctrl* ctrl) {
-  if (kCluster ? tile::try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (true) {
-    if (kCluster ? tile::try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
-    if (sh->abort) return false;
-    if (globaltimer_ns() - t0 > kTimeoutNs) {
-      sh->abort = 1;
-      atomicOr(&ctrl->status, ST_TIMEOUT);
-      return false;
+// time or another role of this CTA gave up.  The clock is read every kPolls tries only: it
+// takes longer than a try, and a wait that polls late holds up the ring.
+// Warps with time to spare sleep between tries, which leaves shared memory to the copies.
+constexpr uint32_t kPolls = 256;
+enum WaitKind { WAIT_HOT, WAIT_IDLE, WAIT_CLUSTER };  // (acquiring what the other CTA released)
+template <WaitKind kKind = WAIT_HOT>
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, Shared* sh, Ctrl* ctrl) {
+  uint64_t t0 = 0;
+  for (uint32_t n = 1;; ++n) {
+    if (kKind == WAIT_CLUSTER ? tile::try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))
+      return true;
+    if (kKind != WAIT_HOT) __nanosleep(64);
+    if (n % kPolls == 0) {
+      if (sh->abort) return false;
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kTimeoutNs) {
+        sh->abort = 1;
+        atomicOr(&ctrl->status, ST_TIMEOUT);
+        return false;
+      }
     }
   }
 }
@@ -292,7 +304,7 @@ __device__ __forceinline__ void store_tokens(const GroupTc& a, uint16_t* out, in
 }
 
 // mapM, mapN: the operand on the M and on the N side (Y: W, X; dX: W, dY; dW: dY, X);
-// mapN16: the N side's in boxes of 16 rows (Y, dX).
+// mapN16: the N side's in boxes of 16 rows (Y, dX), or in blocks of 64 columns (dW).
 template <class T, int kDir>
 __global__ void __launch_bounds__(kThreads<kDir>, 1)
     group_kernel(const __grid_constant__ CUtensorMap mapM, const __grid_constant__ CUtensorMap mapN,
@@ -363,14 +375,22 @@ __global__ void __launch_bounds__(kThreads<kDir>, 1)
           }
           const int d = kb * BK;
           if (kDir == GROUP_DW) {
-            for (int i = 0; i < 2; ++i)
-              tile::tma_load_2d(sm + i * 8192, &mapM, bar, m + i * 64, c.row0 + d);
-            for (int i = 0; i < boxes64; ++i)
-              tile::tma_load_2d(sn + i * 8192, &mapN, bar, c.n0 + rank * half + i * 64,
-                                c.row0 + d);
+            if (a.blocks_m)
+              tile::tma_load_3d(sm, &mapM, bar, 0, c.row0 + d, m / 64);
+            else
+              for (int i = 0; i < 2; ++i)
+                tile::tma_load_2d(sm + i * 8192, &mapM, bar, m + i * 64, c.row0 + d);
+            const int k = c.n0 + rank * half;
+            if (a.blocks_n && half == 128)
+              tile::tma_load_3d(sn, &mapN16, bar, 0, c.row0 + d, k / 64);
+            else
+              for (int i = 0; i < boxes64; ++i)
+                tile::tma_load_2d(sn + i * 8192, &mapN, bar, k + i * 64, c.row0 + d);
           } else {
             if (kDir == GROUP_Y)
               tile::tma_load_3d(sm, &mapM, bar, d, m, c.e);
+            else if (a.blocks_m)
+              tile::tma_load_4d(sm, &mapM, bar, 0, d, m / 64, c.e);
             else
               for (int i = 0; i < 2; ++i)
                 tile::tma_load_3d(sm + i * 8192, &mapM, bar, m + i * 64, d, c.e);
@@ -403,6 +423,9 @@ __global__ void __launch_bounds__(kThreads<kDir>, 1)
       constexpr bool kBf16 = !__is_same(T, __half);
       constexpr uint32_t kMStep = kDir == GROUP_Y ? 2 : 128;  // 16 of the depth, >> 4
       constexpr uint32_t kNStep = kDir == GROUP_DW ? 128 : 2;
+      const uint32_t s0 = smem_u32(smem);
+      const uint64_t md = tile::smem_desc(s0, kDir == GROUP_Y ? 16 : 8192, 1024);
+      const uint64_t nd = tile::smem_desc(s0 + kHalf, kDir == GROUP_DW ? 8192 : 16, 1024);
       int stage = 0, iter = 0;
       uint32_t phase = 0, tphase[2] = {0, 0};
       bool ok = true, any = false;
@@ -415,23 +438,35 @@ __global__ void __launch_bounds__(kThreads<kDir>, 1)
         if (!(ok = wait_on(&sh->tempty[acc], tphase[acc] ^ 1u, sh, a.ctrl))) break;
         tphase[acc] ^= 1u;
         tile::fence_after();
-        for (int kb = 0; kb < c.nkb; ++kb) {
-          if (!(ok = wait_on(&sh->full[stage], phase, sh, a.ctrl))) break;
-          tile::fence_after();
-          const int left = c.depth - kb * BK;
-          const int steps = left >= BK ? BK / 16 : (left + 15) / 16;
-          const uint32_t sm = smem_u32(smem + (size_t)stage * kStageBytes);
-          const uint64_t md = tile::smem_desc(sm, kDir == GROUP_Y ? 16 : 8192, 1024);
-          const uint64_t nd = tile::smem_desc(sm + kHalf, kDir == GROUP_DW ? 8192 : 16, 1024);
-          for (int s = 0; s < steps; ++s)
-            tile::mma_pair(tmem + (uint32_t)(acc * BN), md + (uint64_t)(s * kMStep),
-                           nd + (uint64_t)(s * kNStep), idesc, (kb | s) ? 1u : 0u);
-          any = true;
+        const uint32_t d = tmem + (uint32_t)(acc * BN);
+        uint32_t accumulate = 0;
+        auto step = [&](int s) {
+          tile::mma_pair(d, md + (uint64_t)(stage * (kStageBytes >> 4) + s * kMStep),
+                         nd + (uint64_t)(stage * (kStageBytes >> 4) + s * kNStep), idesc,
+                         accumulate);
+          accumulate = 1;
+        };
+        auto next_stage = [&] {
           tile::commit_pair(&sh->empty[stage], 0x3);
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1u;
           }
+        };
+        any = true;
+        // whole slices unrolled (as a loop of its own: issued a third faster)
+        for (int kb = 0; kb < c.depth / BK; ++kb) {
+          if (!(ok = wait_on(&sh->full[stage], phase, sh, a.ctrl))) break;
+          tile::fence_after();
+#pragma unroll
+          for (int s = 0; s < BK / 16; ++s) step(s);
+          next_stage();
+        }
+        if (ok && c.depth % BK != 0 && (ok = wait_on(&sh->full[stage], phase, sh, a.ctrl))) {
+          tile::fence_after();
+#pragma unroll 1
+          for (int s = 0; s < (c.depth % BK + 15) / 16; ++s) step(s);
+          next_stage();
         }
         if (!ok) break;
         tile::commit_pair(&sh->tfull[acc], 0x3);
@@ -454,7 +489,7 @@ __global__ void __launch_bounds__(kThreads<kDir>, 1)
       if (c.nkb > 0) {
         acc = iter++ & 1;
         int ok = 1;
-        if (lane == 0) ok = wait_on(&sh->tfull[acc], tphase[acc], sh, a.ctrl) ? 1 : 0;
+        if (lane == 0) ok = wait_on<WAIT_IDLE>(&sh->tfull[acc], tphase[acc], sh, a.ctrl) ? 1 : 0;
         if (!__shfl_sync(0xffffffffu, ok, 0)) break;
         tphase[acc] ^= 1u;
         tile::fence_after();
@@ -486,7 +521,7 @@ __global__ void __launch_bounds__(kThreads<kDir>, 1)
       if (c.nkb > 0 && ragged(c, c.nkb - 1)) {
         const int st = (stage + c.nkb - 1) % kStages;
         int ok = 1;
-        if (lane == 0) ok = wait_on(&sh->tail[st], (tails >> st) & 1u, sh, a.ctrl) ? 1 : 0;
+        if (lane == 0) ok = wait_on<WAIT_IDLE>(&sh->tail[st], (tails >> st) & 1u, sh, a.ctrl) ? 1 : 0;
         if (!__shfl_sync(0xffffffffu, ok, 0)) break;
         tails ^= 1u << st;
         const int left = c.depth - (c.nkb - 1) * BK, zr = 16 - (left & 15);
@@ -500,7 +535,7 @@ __global__ void __launch_bounds__(kThreads<kDir>, 1)
         if (lane == 0) {  // the leader's warp passes on that both CTAs' are mended
           if (!leader)
             tile::arrive_cluster(tile::peer_addr(&sh->mend[st], 0));
-          else if (wait_on<true>(&sh->mend[st], mends >> st & 1u, sh, a.ctrl))
+          else if (wait_on<WAIT_CLUSTER>(&sh->mend[st], mends >> st & 1u, sh, a.ctrl))
             mbar_arrive(&sh->full[st]);
         }
         mends ^= 1u << st;
@@ -573,6 +608,23 @@ bool encode(CUtensorMap* map, const Operand& o, uint32_t box_cols, uint32_t box_
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The operand as blocks of 64 columns (its width a multiple of 64), boxes of 64 rows of two
+// blocks; dimensions (64 columns, rows, blocks[, parts]).
+bool encode_blocks(CUtensorMap* map, const Operand& o, bool bf16) {
+  EncodeFn enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dim[4] = {64, (cuuint64_t)o.rows, (cuuint64_t)(o.cols / 64),
+                             (cuuint64_t)o.parts};
+  const cuuint64_t str[3] = {(cuuint64_t)o.ld * 2, 128, (cuuint64_t)o.stride * 2};
+  const cuuint32_t box[4] = {64, 64, 2, 1};
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+             o.parts ? 4 : 3, const_cast<void*>(o.p), dim, str, box, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool tma_ok(const Operand& o) {
   return reinterpret_cast<uintptr_t>(o.p) % 16 == 0 && o.ld % 8 == 0 &&
          (o.parts <= 1 || o.stride % 8 == 0);
@@ -625,15 +677,19 @@ cudaError_t group_typed(const GroupArgs& g, void* ws, Ctx& c) {
   memset(&mm, 0, sizeof(mm));
   memset(&mn, 0, sizeof(mn));
   memset(&mn16, 0, sizeof(mn16));
+  GroupTc a;
+  a.blocks_m = kDir != GROUP_Y && M.cols % 64 == 0;
+  a.blocks_n = kDir == GROUP_DW && N.cols % 64 == 0;
   if (g.rows > 0) {  // (without rows only zeros are stored: no map is used)
     if ((e = pad(M, at, c)) != cudaSuccess || (e = pad(N, at, c)) != cudaSuccess) return e;
-    const bool ok = kDir == GROUP_DW
-                        ? encode(&mm, M, 64, BK, kBf16) && encode(&mn, N, 64, BK, kBf16)
-                        : encode(&mm, M, 64, kDir == GROUP_Y ? 128 : BK, kBf16) &&
-                              encode(&mn, N, BK, 128, kBf16) && encode(&mn16, N, BK, 16, kBf16);
+    bool ok = a.blocks_m ? encode_blocks(&mm, M, kBf16)
+                         : encode(&mm, M, 64, kDir == GROUP_Y ? 128 : BK, kBf16);
+    if (kDir == GROUP_DW)
+      ok = ok && encode(&mn, N, 64, BK, kBf16) && (!a.blocks_n || encode_blocks(&mn16, N, kBf16));
+    else
+      ok = ok && encode(&mn, N, BK, 128, kBf16) && encode(&mn16, N, BK, 16, kBf16);
     if (!ok) return cudaErrorInvalidValue;
   }
-  GroupTc a;
   a.offsets = g.offsets;
   a.rows = (int)g.rows;
   a.groups = (int)g.groups;

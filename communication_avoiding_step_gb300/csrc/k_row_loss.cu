@@ -592,16 +592,17 @@ constexpr size_t kStreamSmem = (size_t)kStages * kStageGranules * 16 + sizeof(St
 // gave up.
 __device__ __forceinline__ bool stage_wait(uint64_t* bar, uint32_t parity, StreamShared* sh,
                                            Ctrl* ctrl) {
-  bool ok = mbar_try_wait(bar, parity);
-  if (!ok) {
-    const uint64_t t0 = globaltimer_ns();
-    while (!(ok = mbar_try_wait(bar, parity))) {
-      if (sh->abort) break;
-      if (globaltimer_ns() - t0 > kTimeoutNs) {
-        sh->abort = 1;
-        atomicOr(&ctrl->status, ST_TIMEOUT);
-        break;
-      }
+  bool ok = false;
+  uint64_t t0 = 0;
+  for (uint32_t n = 1; !(ok = mbar_try_wait(bar, parity)); ++n) {
+    if (n % 256 != 0) continue;  // (reading the clock takes longer than a try)
+    if (sh->abort) break;
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > kTimeoutNs) {
+      sh->abort = 1;
+      atomicOr(&ctrl->status, ST_TIMEOUT);
+      break;
     }
   }
   return __all_sync(0xffffffffu, ok);
