@@ -303,12 +303,17 @@ __device__ __forceinline__ void store_tokens(const GroupTc& a, uint16_t* out, in
   }
 }
 
-// mapM, mapN: the operand on the M and on the N side (Y: W, X; dX: W, dY; dW: dY, X);
-// mapN16: the N side's in boxes of 16 rows (Y, dX), or in blocks of 64 columns (dW).
+// maps.m, maps.n: the operand on the M and on the N side (Y: W, X; dX: W, dY; dW: dY, X).
+// Y, dX: maps.n has boxes of 16, 32, 64, 96 and 128 rows, so that a slice's tokens are one copy
+// whatever the tile's size (a copy costs about 80 cycles of the copy engine beside its
+// bytes); dW: n[0] single blocks of 64 columns, n[1] pairs of them.
+struct Maps {
+  CUtensorMap m;
+  CUtensorMap n[5];
+};
 template <class T, int kDir>
 __global__ void __launch_bounds__(kThreads<kDir>, 1)
-    group_kernel(const __grid_constant__ CUtensorMap mapM, const __grid_constant__ CUtensorMap mapN,
-                 const __grid_constant__ CUtensorMap mapN16, const GroupTc a) {
+    group_kernel(const __grid_constant__ Maps maps, const GroupTc a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~(uintptr_t)1023);
@@ -356,8 +361,9 @@ __global__ void __launch_bounds__(kThreads<kDir>, 1)
         const Tile c = tile_at<kDir>(a, sh, t);
         const int half = c.n / 2;  // this CTA's part of the N side
         const int boxes64 = (half + 63) / 64;
+        const int box = half <= 16 ? 0 : (half + 31) / 32;  // 16, 32, 64, 96 or 128 rows
         const uint32_t bytes =
-            kHalf + (kDir == GROUP_DW ? (uint32_t)boxes64 * 8192 : (uint32_t)half * 128);
+            kHalf + (kDir == GROUP_DW ? boxes64 * 8192u : box ? box * 4096u : 2048u);
         const int m = c.m0 + rank * 128;
         for (int kb = 0; kb < c.nkb; ++kb) {
           if (!wait_on(&sh->empty[stage], phase ^ 1u, sh, a.ctrl)) {
@@ -376,30 +382,25 @@ __global__ void __launch_bounds__(kThreads<kDir>, 1)
           const int d = kb * BK;
           if (kDir == GROUP_DW) {
             if (a.blocks_m)
-              tile::tma_load_3d(sm, &mapM, bar, 0, c.row0 + d, m / 64);
+              tile::tma_load_3d(sm, &maps.m, bar, 0, c.row0 + d, m / 64);
             else
               for (int i = 0; i < 2; ++i)
-                tile::tma_load_2d(sm + i * 8192, &mapM, bar, m + i * 64, c.row0 + d);
+                tile::tma_load_2d(sm + i * 8192, &maps.m, bar, m + i * 64, c.row0 + d);
             const int k = c.n0 + rank * half;
             if (a.blocks_n && half == 128)
-              tile::tma_load_3d(sn, &mapN16, bar, 0, c.row0 + d, k / 64);
+              tile::tma_load_3d(sn, &maps.n[1], bar, 0, c.row0 + d, k / 64);
             else
               for (int i = 0; i < boxes64; ++i)
-                tile::tma_load_2d(sn + i * 8192, &mapN, bar, k + i * 64, c.row0 + d);
+                tile::tma_load_2d(sn + i * 8192, &maps.n[0], bar, k + i * 64, c.row0 + d);
           } else {
             if (kDir == GROUP_Y)
-              tile::tma_load_3d(sm, &mapM, bar, d, m, c.e);
+              tile::tma_load_3d(sm, &maps.m, bar, d, m, c.e);
             else if (a.blocks_m)
-              tile::tma_load_4d(sm, &mapM, bar, 0, d, m / 64, c.e);
+              tile::tma_load_4d(sm, &maps.m, bar, 0, d, m / 64, c.e);
             else
               for (int i = 0; i < 2; ++i)
-                tile::tma_load_3d(sm + i * 8192, &mapM, bar, m + i * 64, d, c.e);
-            const int row = c.row0 + c.n0 + rank * half;
-            if (half == 128)
-              tile::tma_load_2d(sn, &mapN, bar, d, row);
-            else
-              for (int i = 0; i < half / 16; ++i)
-                tile::tma_load_2d(sn + i * 2048, &mapN16, bar, d, row + i * 16);
+                tile::tma_load_3d(sm + i * 8192, &maps.m, bar, m + i * 64, d, c.e);
+            tile::tma_load_2d(sn, &maps.n[box], bar, d, c.row0 + c.n0 + rank * half);
           }
           issued |= 1u << stage;
           last_par = (last_par & ~(1u << stage)) | (phase << stage);
@@ -673,21 +674,22 @@ cudaError_t group_typed(const GroupArgs& g, void* ws, Ctx& c) {
                                : rows_of(g.x, g.rows, g.k, g.ldx);
   char* at = static_cast<char*>(ws) + align_up(sizeof(Ctrl));
   cudaError_t e = cudaSuccess;
-  CUtensorMap mm, mn, mn16;
-  memset(&mm, 0, sizeof(mm));
-  memset(&mn, 0, sizeof(mn));
-  memset(&mn16, 0, sizeof(mn16));
+  Maps maps;
+  memset(&maps, 0, sizeof(maps));
   GroupTc a;
   a.blocks_m = kDir != GROUP_Y && M.cols % 64 == 0;
   a.blocks_n = kDir == GROUP_DW && N.cols % 64 == 0;
   if (g.rows > 0) {  // (without rows only zeros are stored: no map is used)
     if ((e = pad(M, at, c)) != cudaSuccess || (e = pad(N, at, c)) != cudaSuccess) return e;
-    bool ok = a.blocks_m ? encode_blocks(&mm, M, kBf16)
-                         : encode(&mm, M, 64, kDir == GROUP_Y ? 128 : BK, kBf16);
-    if (kDir == GROUP_DW)
-      ok = ok && encode(&mn, N, 64, BK, kBf16) && (!a.blocks_n || encode_blocks(&mn16, N, kBf16));
-    else
-      ok = ok && encode(&mn, N, BK, 128, kBf16) && encode(&mn16, N, BK, 16, kBf16);
+    bool ok = a.blocks_m ? encode_blocks(&maps.m, M, kBf16)
+                         : encode(&maps.m, M, 64, kDir == GROUP_Y ? 128 : BK, kBf16);
+    if (kDir == GROUP_DW) {
+      ok = ok && encode(&maps.n[0], N, 64, BK, kBf16) &&
+           (!a.blocks_n || encode_blocks(&maps.n[1], N, kBf16));
+    } else {
+      for (int i = 0; i < 5; ++i)
+        ok = ok && encode(&maps.n[i], N, BK, i ? 32 * i : 16, kBf16);
+    }
     if (!ok) return cudaErrorInvalidValue;
   }
   a.offsets = g.offsets;
@@ -723,7 +725,7 @@ cudaError_t group_typed(const GroupArgs& g, void* ws, Ctx& c) {
   cfg.numAttrs = 1;
   add_pdl_attr(c, cfg, attr);
   ++c.launches;
-  return cudaLaunchKernelEx(&cfg, fn, mm, mn, mn16, a);
+  return cudaLaunchKernelEx(&cfg, fn, maps, a);
 }
 
 template <class T>
