@@ -21,9 +21,9 @@
 //   warp 0     TMA producer: 64-deep slices of both operands into a ring of stages;
 //   warp 1     (leader) issues the MMAs into one of two TMEM accumulators, so that a
 //              tile's epilogue overlaps the next tile's products;
-//   warps 2-5  epilogue: TMEM -> registers -> one rounding -> shared memory (to turn them
+//   warps 2-9  epilogue: TMEM -> registers -> one rounding -> shared memory (to turn them
 //              into row segments) -> masked stores;
-//   warp 6     (dW) the ragged end of the summed tokens.
+//   warp 10    (dW) the ragged end of the summed tokens.
 //
 // Ragged ends.  In Y and dX rows past a group's end are computed and dropped (a column of
 // the accumulator depends on its own token alone).  In dW only whole steps of 16 tokens are
@@ -51,21 +51,29 @@ inline size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 constexpr int BM = 256, BN = 256, BK = 64;  // tile of a pair
 constexpr int kHalf = 128 * BK * 2;         // a CTA's 128 rows of a slice of one operand
 constexpr int kStageBytes = 2 * kHalf;
-constexpr int kStages = 6;
 constexpr int kMaxGroups = CASGD_MAX_GROUPS;
 constexpr uint64_t kTimeoutNs = 1000000000ull;
-constexpr int kOutBytes = 4 * 32 * 128;  // per epilogue warp: 4 KB
 constexpr uint32_t kTmemCols = 2 * BN;
+// Eight epilogue warps, two per quarter of TMEM's lanes: with four, the short tiles of dW
+// (and stores of Y and dX) waited for their epilogue.
+constexpr int kEpiWarps = 8;
 template <int kDir>
-constexpr int kThreads = kDir == GROUP_DW ? 224 : 192;
+constexpr int kThreads = 32 * (2 + kEpiWarps + (kDir == GROUP_DW ? 1 : 0));
+// Staging per epilogue warp: 32 rows of 128 bytes (dW), or 32 tokens of 64.  dW gives up a
+// stage for it (measured: six stages are no faster than five there).
+template <int kDir>
+constexpr int kStageOut = kDir == GROUP_DW ? 32 * 128 : 32 * 64;
+template <int kDir>
+constexpr int kStages = kDir == GROUP_DW ? 5 : 6;
+constexpr int kMostStages = 6;
 
 struct Shared {
-  uint64_t full[kStages];   // leader: both CTAs' copies of a stage are in
-  uint64_t empty[kStages];  // both: the MMAs have read a stage
-  uint64_t tail[kStages];   // dW, both: this CTA's copies of a ragged slice are in
-  uint64_t mend[kStages];   // dW, leader: the other CTA's are in and mended
-  uint64_t tfull[2];        // both: an accumulator is complete
-  uint64_t tempty[2];       // leader: both CTAs' epilogues are done with it (8 warps)
+  uint64_t full[kMostStages];   // leader: both CTAs' copies of a stage are in
+  uint64_t empty[kMostStages];  // both: the MMAs have read a stage
+  uint64_t tail[kMostStages];   // dW, both: this CTA's copies of a ragged slice are in
+  uint64_t mend[kMostStages];   // dW, leader: the other CTA's are in and mended
+  uint64_t tfull[2];   // both: an accumulator is complete
+  uint64_t tempty[2];  // leader: both CTAs' epilogue warps are done with it
   uint64_t drain;
   uint32_t tmem_base;
   volatile uint32_t abort;
@@ -73,8 +81,11 @@ struct Shared {
   int32_t row0[kMaxGroups + 2];   // first row of each group, held ascending
   int32_t tile0[kMaxGroups + 2];  // first tile of each group
 };
-constexpr size_t kSmemBytes = (size_t)kStages * kStageBytes + kOutBytes + sizeof(Shared) + 1024;
-static_assert(kSmemBytes <= 232448, "dynamic shared memory per CTA");
+template <int kDir>
+constexpr size_t kSmemBytes = (size_t)kStages<kDir> * kStageBytes + kEpiWarps * kStageOut<kDir> +
+                              sizeof(Shared) + 1024;
+static_assert(kSmemBytes<GROUP_Y> <= 232448 && kSmemBytes<GROUP_DW> <= 232448,
+              "dynamic shared memory per CTA");
 
 struct GroupTc {
   const int32_t* offsets;
@@ -213,25 +224,23 @@ __device__ __forceinline__ uint32_t pack2<__half>(uint32_t lo, uint32_t hi) {
   return reinterpret_cast<const uint32_t&>(v);
 }
 
-// Eight 16-bit values, the first `count` of them, to dst.
-__device__ __forceinline__ void store8(uint16_t* dst, uint4 v, int count, bool vec) {
-  if (vec && count >= 8) {
-    *reinterpret_cast<uint4*>(dst) = v;
-    return;
-  }
+// The first `count` of eight 16-bit values to dst, one by one.
+__device__ __forceinline__ void store_some(uint16_t* dst, uint4 v, int count) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int j = 0; j < 8; ++j)
     if (j < count) dst[j] = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
 }
 
-// dW: one warp's 32 rows (n) of a tile, `rows` x `cols` of them real.  64 columns at a
-// time, one row per lane into a staging buffer (16-byte chunk c of row r at slot
-// c ^ (r % 8), so neither side has bank conflicts), then four rows of 128 bytes per store.
+// dW: one warp's 32 rows (n) of a tile, `rows` x `cols` of them real, every other 64
+// columns from c0 on.  One row per lane into a staging buffer (16-byte chunk c of row r at
+// slot c ^ (r % 8), so neither side has bank conflicts), then four rows of 128 bytes per
+// store.
 template <class T>
 __device__ __forceinline__ void store_rows(const GroupTc& a, uint16_t* out, int rows, int cols,
-                                           uint32_t taddr, bool zero, uint8_t* stage, int lane) {
-  for (int c0 = 0; c0 < cols; c0 += 64) {
+                                           int c0, uint32_t taddr, bool zero, uint8_t* stage,
+                                           int lane) {
+  for (; c0 < cols; c0 += 128) {
     uint32_t lo[32], hi[32];
     if (!zero) {
       __syncwarp();
@@ -255,26 +264,34 @@ __device__ __forceinline__ void store_rows(const GroupTc& a, uint16_t* out, int 
       *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) * 16)) = v;
     }
     __syncwarp();
-    const int c = lane & 7, col = c0 + 8 * c;
+    const int c = lane & 7, r0 = lane >> 3;
+    uint16_t* dst = out + (int64_t)r0 * a.ldo + c0 + 8 * c;
+    const int left = cols - c0 - 8 * c;
+    const bool vec = a.vec_out && cols - c0 >= 64;  // (of the whole warp)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = 4 * i + (lane >> 3);
-      if (r < rows && col < cols)
-        store8(out + (int64_t)r * a.ldo + col,
-               *reinterpret_cast<const uint4*>(stage + r * 128 + ((c ^ (r & 7)) * 16)),
-               cols - col, a.vec_out);
+    for (int i = 0; i < 8; ++i, dst += 4 * a.ldo) {
+      const int r = 4 * i + r0;
+      const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((c ^ (r & 7)) * 16));
+      if (r >= rows) continue;
+      if (vec)
+        *reinterpret_cast<uint4*>(dst) = v;
+      else
+        store_some(dst, v, left);
     }
   }
 }
 
-// Y, dX: one warp's 32 columns of the output (TMEM lanes) for `tokens` tokens (TMEM
-// columns), `cols` of them real.  32 tokens at a time, a lane's column of each into the
+// Y, dX: one warp's 32 columns of the output (TMEM lanes), `cols` of them real, for every
+// other 32 tokens (TMEM columns) from t0 on.  A lane's column of each token into the
 // staging buffer, then eight tokens' 64-byte segments per store.
 template <class T>
 __device__ __forceinline__ void store_tokens(const GroupTc& a, uint16_t* out, int tokens, int cols,
-                                             uint32_t taddr, bool zero, uint8_t* stage, int lane) {
+                                             int t0, uint32_t taddr, bool zero, uint8_t* stage,
+                                             int lane) {
   uint16_t* st = reinterpret_cast<uint16_t*>(stage);
-  for (int t0 = 0; t0 < tokens; t0 += 32) {
+  const int col = (lane & 3) * 8;
+  const bool vec = a.vec_out && cols >= 32;  // (of the whole warp)
+  for (; t0 < tokens; t0 += 64) {
     uint32_t v[32];
     if (!zero) {
       __syncwarp();
@@ -292,18 +309,20 @@ __device__ __forceinline__ void store_tokens(const GroupTc& a, uint16_t* out, in
       st[(e + 1) * 32 + lane] = (uint16_t)(p >> 16);
     }
     __syncwarp();
-    const int col = (lane & 3) * 8;
+    uint16_t* dst = out + (int64_t)(t0 + (lane >> 2)) * a.ldo + col;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 4; ++i, dst += 8 * a.ldo) {
       const int t = 8 * i + (lane >> 2);
-      if (t0 + t < tokens && col < cols)
-        store8(out + (int64_t)(t0 + t) * a.ldo + col,
-               *reinterpret_cast<const uint4*>(st + t * 32 + col), cols - col, a.vec_out);
+      const uint4 w = *reinterpret_cast<const uint4*>(st + t * 32 + col);
+      if (t0 + t >= tokens) continue;
+      if (vec)
+        *reinterpret_cast<uint4*>(dst) = w;
+      else
+        store_some(dst, w, cols - col);
     }
   }
 }
 
-// maps.m, maps.n: the operand on the M and on the N side (Y: W, X; dX: W, dY; dW: dY, X).
 // Y, dX: maps.n has boxes of 16, 32, 64, 96 and 128 rows, so that a slice's tokens are one copy
 // whatever the tile's size (a copy costs about 80 cycles of the copy engine beside its
 // bytes); dW: n[0] single blocks of 64 columns, n[1] pairs of them.
@@ -317,14 +336,15 @@ __global__ void __launch_bounds__(kThreads<kDir>, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~(uintptr_t)1023);
-  uint8_t* out_stage = smem + (size_t)kStages * kStageBytes;
-  Shared* sh = reinterpret_cast<Shared*>(out_stage + kOutBytes);
+  constexpr int kSt = kStages<kDir>;
+  uint8_t* out_stage = smem + (size_t)kSt * kStageBytes;
+  Shared* sh = reinterpret_cast<Shared*>(out_stage + kEpiWarps * kStageOut<kDir>);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)tile::cluster_rank();
   const bool leader = rank == 0;
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kSt; ++i) {
       mbar_init(&sh->full[i], 1);
       mbar_init(&sh->empty[i], 1);
       mbar_init(&sh->tail[i], 1);
@@ -332,7 +352,7 @@ __global__ void __launch_bounds__(kThreads<kDir>, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh->tfull[i], 1);
-      mbar_init(&sh->tempty[i], 8);
+      mbar_init(&sh->tempty[i], 2 * kEpiWarps);
     }
     mbar_init(&sh->drain, 1);
     sh->abort = 0;
@@ -404,14 +424,14 @@ __global__ void __launch_bounds__(kThreads<kDir>, 1)
           }
           issued |= 1u << stage;
           last_par = (last_par & ~(1u << stage)) | (phase << stage);
-          if (++stage == kStages) {
+          if (++stage == kSt) {
             stage = 0;
             phase ^= 1u;
           }
         }
       }
       // every copy of the pair has landed before the CTAs may exit
-      for (int st = 0; st < kStages && leader; ++st)
+      for (int st = 0; st < kSt && leader; ++st)
         if (issued & (1u << st)) {
           const uint64_t t0 = globaltimer_ns();
           while (!mbar_try_wait(&sh->full[st], (last_par >> st) & 1u) &&
@@ -449,7 +469,7 @@ __global__ void __launch_bounds__(kThreads<kDir>, 1)
         };
         auto next_stage = [&] {
           tile::commit_pair(&sh->empty[stage], 0x3);
-          if (++stage == kStages) {
+          if (++stage == kSt) {
             stage = 0;
             phase ^= 1u;
           }
@@ -479,9 +499,10 @@ __global__ void __launch_bounds__(kThreads<kDir>, 1)
         }
       }
     }
-  } else if (warp < 6) {
+  } else if (warp < 2 + kEpiWarps) {
     const int quarter = warp & 3;  // TMEM lanes 32 * quarter .. + 31
-    uint8_t* stage = out_stage + (warp - 2) * (32 * 128);
+    const int half = (warp - 2) >> 2;  // which of the quarter's two warps
+    uint8_t* stage = out_stage + (warp - 2) * kStageOut<kDir>;
     int iter = 0;
     uint32_t tphase[2] = {0, 0};
     for (int t = pair; t < tiles; t += pairs) {
@@ -501,10 +522,10 @@ __global__ void __launch_bounds__(kThreads<kDir>, 1)
       if (m_left > 0) {
         if (kDir == GROUP_DW)
           store_rows<T>(a, a.out + c.e * a.stride_o + (int64_t)m * a.ldo + c.n0, m_left, c.valid,
-                        taddr, c.nkb == 0, stage, lane);
+                        64 * half, taddr, c.nkb == 0, stage, lane);
         else
-          store_tokens<T>(a, a.out + (int64_t)(c.row0 + c.n0) * a.ldo + m, c.valid, m_left, taddr,
-                          c.nkb == 0, stage, lane);
+          store_tokens<T>(a, a.out + (int64_t)(c.row0 + c.n0) * a.ldo + m, c.valid, m_left,
+                          32 * half, taddr, c.nkb == 0, stage, lane);
       }
       if (c.nkb > 0) {
         tile::fence_before();
@@ -520,7 +541,7 @@ __global__ void __launch_bounds__(kThreads<kDir>, 1)
     for (int t = pair; t < tiles; t += pairs) {
       const Tile c = tile_at<kDir>(a, sh, t);
       if (c.nkb > 0 && ragged(c, c.nkb - 1)) {
-        const int st = (stage + c.nkb - 1) % kStages;
+        const int st = (stage + c.nkb - 1) % kSt;
         int ok = 1;
         if (lane == 0) ok = wait_on<WAIT_IDLE>(&sh->tail[st], (tails >> st) & 1u, sh, a.ctrl) ? 1 : 0;
         if (!__shfl_sync(0xffffffffu, ok, 0)) break;
@@ -541,7 +562,7 @@ __global__ void __launch_bounds__(kThreads<kDir>, 1)
         }
         mends ^= 1u << st;
       }
-      stage = (stage + c.nkb) % kStages;
+      stage = (stage + c.nkb) % kSt;
     }
   }
   tile::fence_before();
@@ -709,7 +730,7 @@ cudaError_t group_typed(const GroupArgs& g, void* ws, Ctx& c) {
   const int64_t most = kDir == GROUP_DW ? g.groups * mt * ((g.k + BN - 1) / BN)
                                         : (g.rows / BN + some + 1) * mt;
   const auto fn = group_kernel<T, kDir>;
-  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes<kDir>);
   if (e != cudaSuccess) return e;
   const int64_t pairs = c.num_sms / 2;
   cudaLaunchConfig_t cfg = {};
@@ -719,7 +740,7 @@ cudaError_t group_typed(const GroupArgs& g, void* ws, Ctx& c) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.gridDim = dim3((unsigned)(2 * (most < pairs ? most : pairs)));
   cfg.blockDim = dim3(kThreads<kDir>);
-  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.dynamicSmemBytes = kSmemBytes<kDir>;
   cfg.stream = c.stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
