@@ -23,13 +23,15 @@
 //              tile's epilogue overlaps the next tile's products;
 //   warps 2-9  epilogue: TMEM -> registers -> one rounding -> shared memory (to turn them
 //              into row segments) -> masked stores;
-//   warp 10    (dW) the ragged end of the summed tokens.
+//   warp 10    (dW) the last tokens of a group.
 //
 // Ragged ends.  In Y and dX rows past a group's end are computed and dropped (a column of
-// the accumulator depends on its own token alone).  In dW only whole steps of 16 tokens are
-// issued, and the tokens past the end in the last step, which are other groups', are set to
-// zero in both operands in shared memory first, since zero times another group's infinity
-// would not be zero.
+// the accumulator depends on its own token alone).  In dW a group's last 1 to 15 tokens, if
+// it is no multiple of 16 (the MMA's step), go through buffers of their own: a warp
+// copies 16 tokens, sets those past the end, which are other groups', to zero in both
+// operands (zero times another group's infinity would not be zero) and passes the buffer
+// on.  It works up to two tiles ahead; mending the last slice in the ring instead held up the
+// tensor cores by 2 us a tile.
 // The operand layouts: k runs along the 128-byte rows of both operands in Y; in dX the
 // weights are summed over their rows (n), in dW both operands over theirs, which the MMA
 // takes as MN-major operands, so nothing is transposed in memory.
@@ -59,6 +61,8 @@ constexpr uint32_t kTmemCols = 2 * BN;
 constexpr int kEpiWarps = 8;
 template <int kDir>
 constexpr int kThreads = 32 * (2 + kEpiWarps + (kDir == GROUP_DW ? 1 : 0));
+constexpr int kTails = 3;                       // buffers for a group's last tokens,
+constexpr int kTailBytes = 2 * 16 * 128 * 2;  // 16 of a CTA's halves of both sides
 // Staging per epilogue warp: 32 rows of 128 bytes (dW), or 32 tokens of 64.  dW gives up a
 // stage for it (measured: six stages are no faster than five there).
 template <int kDir>
@@ -70,8 +74,9 @@ constexpr int kMostStages = 6;
 struct Shared {
   uint64_t full[kMostStages];   // leader: both CTAs' copies of a stage are in
   uint64_t empty[kMostStages];  // both: the MMAs have read a stage
-  uint64_t tail[kMostStages];   // dW, both: this CTA's copies of a ragged slice are in
-  uint64_t mend[kMostStages];   // dW, leader: the other CTA's are in and mended
+  // dW, last tokens of a group: this CTA's copies are in (both CTAs), both
+  // CTAs' are in and mended (leader), the MMA has read them (both)
+  uint64_t tail[kTails], mended[kTails], used[kTails];
   uint64_t tfull[2];   // both: an accumulator is complete
   uint64_t tempty[2];  // leader: both CTAs' epilogue warps are done with it
   uint64_t drain;
@@ -83,7 +88,7 @@ struct Shared {
 };
 template <int kDir>
 constexpr size_t kSmemBytes = (size_t)kStages<kDir> * kStageBytes + kEpiWarps * kStageOut<kDir> +
-                              sizeof(Shared) + 1024;
+                              (kDir == GROUP_DW ? kTails * kTailBytes : 0) + sizeof(Shared) + 1024;
 static_assert(kSmemBytes<GROUP_Y> <= 232448 && kSmemBytes<GROUP_DW> <= 232448,
               "dynamic shared memory per CTA");
 
@@ -184,7 +189,9 @@ struct Tile {
   int e, row0, rows;  // group and its rows
   int m0;             // first index of the weights' dimension on the M side
   int n0, n, valid;   // N side: first token of the group (dW: first k), MMA size, real size
-  int depth, nkb;     // summed length and its 64-deep slices (0: the tile is zeros)
+  int depth, nkb;     // summed length and its 64-deep slices
+  int last;           // dW: tokens after the last whole step of 16 (not part of depth)
+  __device__ __forceinline__ bool zero() const { return nkb == 0 && last == 0; }
 };
 
 template <int kDir>
@@ -206,7 +213,8 @@ __device__ __forceinline__ Tile tile_at(const GroupTc& a, const Shared* sh, int 
   r.n0 = local % nt * step;
   r.valid = len - r.n0 < step ? len - r.n0 : step;
   r.n = (r.valid + 31) & ~31;
-  r.depth = kDir == GROUP_Y ? a.k : kDir == GROUP_DX ? a.n : r.rows;
+  r.depth = kDir == GROUP_Y ? a.k : kDir == GROUP_DX ? a.n : r.rows & ~15;
+  r.last = kDir == GROUP_DW ? r.rows & 15 : 0;
   r.nkb = kDir != GROUP_DW && lo == a.groups ? 0 : (r.depth + BK - 1) / BK;
   return r;
 }
@@ -325,7 +333,8 @@ __device__ __forceinline__ void store_tokens(const GroupTc& a, uint16_t* out, in
 
 // Y, dX: maps.n has boxes of 16, 32, 64, 96 and 128 rows, so that a slice's tokens are one copy
 // whatever the tile's size (a copy costs about 80 cycles of the copy engine beside its
-// bytes); dW: n[0] single blocks of 64 columns, n[1] pairs of them.
+// bytes); dW: n[0] single blocks of 64 columns, n[1] pairs of them, n[2] blocks of 16 rows,
+// n[3] such blocks of the M side's operand.
 struct Maps {
   CUtensorMap m;
   CUtensorMap n[5];
@@ -338,7 +347,9 @@ __global__ void __launch_bounds__(kThreads<kDir>, 1)
                                              ~(uintptr_t)1023);
   constexpr int kSt = kStages<kDir>;
   uint8_t* out_stage = smem + (size_t)kSt * kStageBytes;
-  Shared* sh = reinterpret_cast<Shared*>(out_stage + kEpiWarps * kStageOut<kDir>);
+  uint8_t* tail_buf = out_stage + kEpiWarps * kStageOut<kDir>;  // (dW; 1024-byte aligned)
+  Shared* sh =
+      reinterpret_cast<Shared*>(tail_buf + (kDir == GROUP_DW ? kTails * kTailBytes : 0));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)tile::cluster_rank();
   const bool leader = rank == 0;
@@ -347,12 +358,15 @@ __global__ void __launch_bounds__(kThreads<kDir>, 1)
     for (int i = 0; i < kSt; ++i) {
       mbar_init(&sh->full[i], 1);
       mbar_init(&sh->empty[i], 1);
-      mbar_init(&sh->tail[i], 1);
-      mbar_init(&sh->mend[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh->tfull[i], 1);
       mbar_init(&sh->tempty[i], 2 * kEpiWarps);
+    }
+    for (int i = 0; i < kTails; ++i) {
+      mbar_init(&sh->tail[i], 1);
+      mbar_init(&sh->mended[i], 2);
+      mbar_init(&sh->used[i], 1);
     }
     mbar_init(&sh->drain, 1);
     sh->abort = 0;
@@ -367,11 +381,6 @@ __global__ void __launch_bounds__(kThreads<kDir>, 1)
   tile::fence_after();
   const uint32_t tmem = sh->tmem_base;
   const int tiles = sh->tiles;
-  // dW: whether slice kb of a tile ends inside a step of 16
-  auto ragged = [](const Tile& c, int kb) {
-    return kDir == GROUP_DW && kb == c.nkb - 1 && (c.depth & 15) != 0;
-  };
-
   if (warp == 0) {
     if (lane == 0) {
       int stage = 0;
@@ -391,14 +400,8 @@ __global__ void __launch_bounds__(kThreads<kDir>, 1)
             break;
           }
           const uint32_t sm = smem_u32(smem + (size_t)stage * kStageBytes), sn = sm + kHalf;
-          const uint32_t lead = tile::peer_addr(&sh->full[stage], 0);
-          uint32_t bar = lead;
-          if (ragged(c, kb)) {
-            bar = tile::peer_addr(&sh->tail[stage], rank);
-            mbar_expect_tx(&sh->tail[stage], bytes);
-          } else if (leader) {
-            mbar_expect_tx(&sh->full[stage], 2 * bytes);
-          }
+          const uint32_t bar = tile::peer_addr(&sh->full[stage], 0);
+          if (leader) mbar_expect_tx(&sh->full[stage], 2 * bytes);
           const int d = kb * BK;
           if (kDir == GROUP_DW) {
             if (a.blocks_m)
@@ -448,11 +451,11 @@ __global__ void __launch_bounds__(kThreads<kDir>, 1)
       const uint64_t md = tile::smem_desc(s0, kDir == GROUP_Y ? 16 : 8192, 1024);
       const uint64_t nd = tile::smem_desc(s0 + kHalf, kDir == GROUP_DW ? 8192 : 16, 1024);
       int stage = 0, iter = 0;
-      uint32_t phase = 0, tphase[2] = {0, 0};
+      uint32_t phase = 0, tphase[2] = {0, 0}, tails = 0;
       bool ok = true, any = false;
       for (int t = pair; t < tiles && ok; t += pairs) {
         const Tile c = tile_at<kDir>(a, sh, t);
-        if (c.nkb == 0) continue;
+        if (c.zero()) continue;
         const uint32_t idesc =
             tile::instr_desc(BM, c.n, kBf16, kDir != GROUP_Y, kDir == GROUP_DW);
         const int acc = iter++ & 1;
@@ -489,6 +492,17 @@ __global__ void __launch_bounds__(kThreads<kDir>, 1)
           for (int s = 0; s < (c.depth % BK + 15) / 16; ++s) step(s);
           next_stage();
         }
+        if (kDir == GROUP_DW && ok && c.last) {
+          const int b = tails % kTails;
+          if ((ok = wait_on<WAIT_CLUSTER>(&sh->mended[b], tails / kTails & 1u, sh, a.ctrl))) {
+            tile::fence_after();
+            const uint32_t sm = smem_u32(tail_buf + b * kTailBytes);
+            tile::mma_pair(d, tile::smem_desc(sm, 2048, 1024),
+                           tile::smem_desc(sm + kTailBytes / 2, 2048, 1024), idesc, accumulate);
+            tile::commit_pair(&sh->used[b], 0x3);
+            ++tails;
+          }
+        }
         if (!ok) break;
         tile::commit_pair(&sh->tfull[acc], 0x3);
       }
@@ -508,7 +522,7 @@ __global__ void __launch_bounds__(kThreads<kDir>, 1)
     for (int t = pair; t < tiles; t += pairs) {
       const Tile c = tile_at<kDir>(a, sh, t);
       int acc = 0;
-      if (c.nkb > 0) {
+      if (!c.zero()) {
         acc = iter++ & 1;
         int ok = 1;
         if (lane == 0) ok = wait_on<WAIT_IDLE>(&sh->tfull[acc], tphase[acc], sh, a.ctrl) ? 1 : 0;
@@ -522,47 +536,51 @@ __global__ void __launch_bounds__(kThreads<kDir>, 1)
       if (m_left > 0) {
         if (kDir == GROUP_DW)
           store_rows<T>(a, a.out + c.e * a.stride_o + (int64_t)m * a.ldo + c.n0, m_left, c.valid,
-                        64 * half, taddr, c.nkb == 0, stage, lane);
+                        64 * half, taddr, c.zero(), stage, lane);
         else
           store_tokens<T>(a, a.out + (int64_t)(c.row0 + c.n0) * a.ldo + m, c.valid, m_left,
-                          32 * half, taddr, c.nkb == 0, stage, lane);
+                          32 * half, taddr, c.zero(), stage, lane);
       }
-      if (c.nkb > 0) {
+      if (!c.zero()) {
         tile::fence_before();
         __syncwarp();
         if (lane == 0) tile::arrive_cluster(tile::peer_addr(&sh->tempty[acc], 0));
       }
     }
   } else if (kDir == GROUP_DW) {
-    // The ragged slices: once this CTA's copies are in, zeros to the tokens past the
-    // group's end in the last step, in every 64-column block of both operands.
-    int stage = 0;
-    uint32_t tails = 0, mends = 0;  // parity of the next use of each stage's barriers
+    // The last tokens: 16 of them, zeros past the group's end, in every 64-column block.
+    uint32_t tails = 0;
     for (int t = pair; t < tiles; t += pairs) {
       const Tile c = tile_at<kDir>(a, sh, t);
-      if (c.nkb > 0 && ragged(c, c.nkb - 1)) {
-        const int st = (stage + c.nkb - 1) % kSt;
-        int ok = 1;
-        if (lane == 0) ok = wait_on<WAIT_IDLE>(&sh->tail[st], (tails >> st) & 1u, sh, a.ctrl) ? 1 : 0;
-        if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-        tails ^= 1u << st;
-        const int left = c.depth - (c.nkb - 1) * BK, zr = 16 - (left & 15);
-        const int blocks = 2 + (c.n / 2 + 63) / 64;
-        uint8_t* sp = smem + (size_t)st * kStageBytes;
-        for (int i = lane; i < blocks * zr * 8; i += 32)
-          *reinterpret_cast<uint4*>(sp + i / (zr * 8) * 8192 + (left + i / 8 % zr) * 128 +
-                                    (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-        tile::fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {  // the leader's warp passes on that both CTAs' are mended
-          if (!leader)
-            tile::arrive_cluster(tile::peer_addr(&sh->mend[st], 0));
-          else if (wait_on<WAIT_CLUSTER>(&sh->mend[st], mends >> st & 1u, sh, a.ctrl))
-            mbar_arrive(&sh->full[st]);
+      if (c.last == 0) continue;
+      const int b = tails % kTails, half = c.n / 2, nb = (half + 63) / 64;
+      const uint32_t par = tails / kTails & 1u;
+      uint8_t* buf = tail_buf + b * kTailBytes;
+      int ok = 1;
+      if (lane == 0) {
+        ok = wait_on<WAIT_IDLE>(&sh->used[b], par ^ 1u, sh, a.ctrl) ? 1 : 0;
+        if (ok) {
+          const uint32_t bar = tile::peer_addr(&sh->tail[b], rank), sm = smem_u32(buf);
+          const int row = c.row0 + c.depth;
+          mbar_expect_tx(&sh->tail[b], (uint32_t)(2 + nb) * 2048);
+          for (int i = 0; i < 2; ++i)
+            tile::tma_load_2d(sm + i * 2048, &maps.n[3], bar, c.m0 + rank * 128 + i * 64, row);
+          for (int i = 0; i < nb; ++i)
+            tile::tma_load_2d(sm + kTailBytes / 2 + i * 2048, &maps.n[2], bar,
+                              c.n0 + rank * half + i * 64, row);
+          ok = wait_on(&sh->tail[b], par, sh, a.ctrl) ? 1 : 0;
         }
-        mends ^= 1u << st;
       }
-      stage = (stage + c.nkb) % kSt;
+      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+      __syncwarp();
+      const int zr = 16 - c.last;
+      for (int i = lane; i < (2 + nb) * zr * 8; i += 32)
+        *reinterpret_cast<uint4*>(buf + i / (zr * 8) * 2048 + (c.last + i / 8 % zr) * 128 +
+                                  (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+      tile::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) tile::arrive_cluster(tile::peer_addr(&sh->mended[b], 0));
+      ++tails;
     }
   }
   tile::fence_before();
@@ -706,6 +724,7 @@ cudaError_t group_typed(const GroupArgs& g, void* ws, Ctx& c) {
                          : encode(&maps.m, M, 64, kDir == GROUP_Y ? 128 : BK, kBf16);
     if (kDir == GROUP_DW) {
       ok = ok && encode(&maps.n[0], N, 64, BK, kBf16) &&
+           encode(&maps.n[2], N, 64, 16, kBf16) && encode(&maps.n[3], M, 64, 16, kBf16) &&
            (!a.blocks_n || encode_blocks(&maps.n[1], N, kBf16));
     } else {
       for (int i = 0; i < 5; ++i)
