@@ -10,6 +10,7 @@
 // and a run that crosses chunk borders is joined from the chunks' partial sums in
 // ascending order.  Chunks of equal length keep the work even when one token makes up
 // most of the batch.
+#include "ptx_async.cuh"
 #include "token_common.cuh"
 
 namespace casgd {
@@ -116,6 +117,7 @@ constexpr int kTile = kSortThreads * kSortItems;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxRadix = 512;
 constexpr int kMaxCluster = 8;
+constexpr int kMaxChunk = 64;  // pairs that one group of threads sums
 
 struct SortPlan {
   int passes, bits;  // digits of `bits` bits
@@ -138,9 +140,10 @@ struct GradLayout {
 GradLayout grad_layout(int64_t rows, int64_t vocab, int64_t dim) {
   GradLayout L;
   L.tiles = rows > 0 ? (rows + kTile - 1) / kTile : 1;
-  // Chunk length: enough chunks to fill the GPU, few enough partial sums for long lists.
+  // Chunk length: enough chunks to fill the GPU, few enough partial sums for long lists
+  // (60,000 tokens of 2048 columns: 136 us with up to 2048 chunks, 166 us with up to 4096).
   L.chunk = 8;
-  while (L.chunk < 64 && rows / L.chunk > 4096) L.chunk *= 2;
+  while (L.chunk < kMaxChunk && rows / L.chunk > 2048) L.chunk *= 2;
   L.chunks = (rows + L.chunk - 1) / L.chunk;
   const SortPlan p = sort_plan(vocab);
   size_t o = align_up(sizeof(Ctrl));
@@ -453,119 +456,214 @@ __device__ __forceinline__ void put_row(TG* g, const float* s, float scale, bool
   *p = o;
 }
 
-// blockDim (tx, ty): ty chunks; tx threads share a chunk's columns, each with kJ groups of
-// kV consecutive columns, the groups tx * kV apart (kV = 1, kJ = 8 where rows do not start
-// on 16-byte boundaries: as many loads in flight per token as one wide load brings).
-template <class TD, class TG, int kV, int kJ>
-__global__ void __launch_bounds__(128) grad_sum_kernel(GradArgs a, const TD* dout, TG* grad) {
+// blockDim (tx, ty): ty chunks, of each a slab of tx * kV columns, kV = 16 / sizeof(TD) per
+// thread: consecutive ones (kVec), or tx apart where rows do not start on 16-byte
+// boundaries.  Rows come through shared memory by bulk copies, kBatch rows of each chunk at
+// a time and (chunks of more than one batch) two batches in turn: copies hold tens of KB
+// per block in flight, which loads into registers did not (16 warps' worth).  A bulk copy
+// moves whole 16-byte granules; what a row's slab has of other granules (up to 15 bytes at
+// either end) is loaded element by element, so nothing outside the row is read.
+constexpr int kSumThreads = 128, kMinTx = 8, kBatch = 8;
+__host__ __device__ constexpr int slab_pitch(int tx) { return tx * 16 + 32; }
+
+template <class TD, class TG, bool kVec>
+__global__ void __launch_bounds__(kSumThreads) grad_sum_kernel(GradArgs a, const TD* dout,
+                                                               TG* grad, Ctrl* ctrl) {
+  constexpr int kV = 16 / (int)sizeof(TD);
+  extern __shared__ __align__(16) uint8_t rows_smem[];
+  __shared__ uint32_t keys[kSumThreads / kMinTx][kMaxChunk];
+  __shared__ uint32_t places[kSumThreads / kMinTx][kMaxChunk];
+  __shared__ uint64_t landed[2];
+  const int tx = blockDim.x, ty = blockDim.y, x = threadIdx.x, y = threadIdx.y;
+  const int tid = y * tx + x;
+  if (tid == 0) {
+    mbar_init(&landed[0], kBatch * ty);
+    mbar_init(&landed[1], kBatch * ty);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
   wait_prior_grid();
   allow_next_grid();
-  const int64_t span = (int64_t)blockDim.x * kV;
-  const int64_t slabs = (a.dim + span * kJ - 1) / (span * kJ);
+  const int span = tx * kV;
+  const int64_t slabs = (a.dim + span - 1) / span;
   const int64_t slab = blockIdx.x % slabs;
-  const int64_t c = blockIdx.x / slabs * blockDim.y + threadIdx.y;
-  const int64_t col = slab * span * kJ + threadIdx.x * kV;
-  if (c >= a.chunks || col >= a.dim) return;
-  const int groups = (int)((a.dim - col + span - 1) / span);  // of this thread, up to kJ
-  const int64_t i0 = c * a.chunk, i1 = i0 + a.chunk < a.rows ? i0 + a.chunk : a.rows;
-  const uint32_t before = i0 > 0 ? a.key[i0 - 1] : 0xffffffffu;
-  const uint32_t after = i1 < a.rows ? a.key[i1] : 0xffffffffu;
-  float s[kJ][kV];
-#pragma unroll
-  for (int g = 0; g < kJ; ++g)
-#pragma unroll
-    for (int e = 0; e < kV; ++e) s[g][e] = 0.0f;
-  int64_t start = i0;  // of the run being summed
-  constexpr int kU = kJ > 1 ? 2 : 4;
-  for (int64_t i = i0; i < i1; i += kU) {
-    Pack<TD, kV> v[kU][kJ];
-    uint32_t k[kU];
-#pragma unroll
-    for (int j = 0; j < kU; ++j) {
-      k[j] = i + j < i1 ? a.key[i + j] : (uint32_t)a.vocab;
-      if (k[j] < (uint32_t)a.vocab) {
-        const TD* src = dout + (int64_t)a.pos[i + j] * a.ldd + col;
-#pragma unroll
-        for (int g = 0; g < kJ; ++g)
-          if (kJ == 1 || g < groups)
-            v[j][g] = *reinterpret_cast<const Pack<TD, kV>*>(src + g * span);
+  const int64_t c = blockIdx.x / slabs * ty + y;
+  const int64_t col0 = slab * span;
+  const int width = (int)(a.dim - col0 < span ? a.dim - col0 : span);
+  const int64_t i0 = c * a.chunk;
+  const int n = c >= a.chunks ? 0 : (int)(i0 + a.chunk < a.rows ? a.chunk : a.rows - i0);
+  const uint32_t* key = keys[y];
+  const uint32_t* place = places[y];
+  for (int i = x; i < n; i += tx) {
+    keys[y][i] = a.key[i0 + i];
+    places[y][i] = a.pos[i0 + i];
+  }
+  const uint32_t before = n > 0 && i0 > 0 ? a.key[i0 - 1] : 0xffffffffu;
+  const uint32_t after = n > 0 && i0 + n < a.rows ? a.key[i0 + n] : 0xffffffffu;
+  __syncthreads();
+  const int pitch = slab_pitch(tx);
+  const int batches = (int)((a.chunk + kBatch - 1) / kBatch);
+  // row r of a batch: its slab's first byte lies at the same offset within 16 in both
+  auto row_buf = [&](int buf, int r) { return rows_smem + ((buf * ty + y) * kBatch + r) * pitch; };
+  auto fetch = [&](int batch) {
+    const int buf = batch & 1;
+    for (int r = x; r < kBatch; r += tx) {
+      const int i = batch * kBatch + r;
+      uint32_t bytes = 0;
+      if (i < n && key[i] < (uint32_t)a.vocab) {
+        const uintptr_t p =
+            reinterpret_cast<uintptr_t>(dout + (int64_t)place[i] * a.ldd + col0);
+        const uintptr_t p0 = (p + 15) & ~(uintptr_t)15,
+                        p1 = (p + width * sizeof(TD)) & ~(uintptr_t)15;
+        if (p1 > p0) {
+          bytes = (uint32_t)(p1 - p0);
+          mbar_expect_tx(&landed[buf], bytes);
+          bulk_load(row_buf(buf, r) + (p0 - (p & ~(uintptr_t)15)),
+                    reinterpret_cast<const void*>(p0), bytes, &landed[buf]);
+        }
+      }
+      if (!bytes) mbar_arrive(&landed[buf]);
+    }
+    // the elements outside whole granules (none where rows are aligned)
+    for (int l = x; !kVec && l < kBatch * 16; l += tx) {
+      const int r = l >> 4, i = batch * kBatch + r;
+      if (i >= n || key[i] >= (uint32_t)a.vocab) continue;
+      const TD* src = dout + (int64_t)place[i] * a.ldd + col0;
+      const uintptr_t p = reinterpret_cast<uintptr_t>(src);
+      int head = (int)(((0 - p) & 15) / sizeof(TD));
+      if (head > width) head = width;
+      const int edge = head + (width - head) % kV;  // elements outside whole granules
+      TD* dst = reinterpret_cast<TD*>(row_buf(buf, r) + (p & 15));
+      if ((l & 15) < edge) {
+        const int e = (l & 15) < head ? l & 15 : width - edge + (l & 15);
+        dst[e] = src[e];
       }
     }
+  };
+  fetch(0);
+  const int mine = kVec ? x * kV : x, step = kVec ? 1 : tx;  // this thread's columns
+  float s[kV];
 #pragma unroll
-    for (int j = 0; j < kU; ++j) {
-      if (k[j] >= (uint32_t)a.vocab) break;  // dropped tokens sort last
+  for (int e = 0; e < kV; ++e) s[e] = 0.0f;
+  int start = 0;  // of the run being summed
+  for (int batch = 0; batch < batches; ++batch) {
+    if (batch + 1 < batches) fetch(batch + 1);
+    uint64_t t0 = 0;
+    for (uint32_t m = 1; !mbar_try_wait(&landed[batch & 1], batch >> 1 & 1u); ++m) {
+      if (m % 256 != 0) continue;
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > 1000000000ull) {  // a copy that did not land in a second: reported
+        set_status(ctrl, ST_TIMEOUT);
+        break;
+      }
+    }
+    __syncthreads();  // (the elements at the edges)
+    const int end = n - batch * kBatch < kBatch ? n - batch * kBatch : kBatch;
+    for (int r = 0; r < end && mine < width; ++r) {
+      const int i = batch * kBatch + r;
+      const uint32_t k = key[i];
+      if (k >= (uint32_t)a.vocab) break;  // dropped tokens sort last
+      const uint8_t* row = row_buf(batch & 1, r);
+      if (kVec) {
+        const Pack<TD, kV> v = *reinterpret_cast<const Pack<TD, kV>*>(row + x * 16);
 #pragma unroll
-      for (int g = 0; g < kJ; ++g)
+        for (int e = 0; e < kV; ++e) s[e] += Elem<TD>::get(v.v[e]);
+      } else {
+        const TD* src = reinterpret_cast<const TD*>(
+            row + (reinterpret_cast<uintptr_t>(dout + (int64_t)place[i] * a.ldd + col0) & 15));
 #pragma unroll
         for (int e = 0; e < kV; ++e)
-          if (kJ == 1 || g < groups) s[g][e] += Elem<TD>::get(v[j][g].v[e]);
-      const bool last = i + j + 1 == i1;
-      const uint32_t nk = last ? after : j + 1 < kU ? k[j + 1 < kU ? j + 1 : 0] : a.key[i + kU];
-      if (!last && nk == k[j]) continue;
+          if (mine + e * step < width) s[e] += Elem<TD>::get(src[mine + e * step]);
+      }
+      const bool last = i + 1 == n;
+      if (!last && key[i + 1] == k) continue;
       // the run ends here, or the chunk does
-      const bool from = start == i0 && before == k[j];
-      const bool on = last && after == k[j];
-#pragma unroll
-      for (int g = 0; g < kJ; ++g) {
-        if (kJ > 1 && g >= groups) break;
+      const bool from = start == 0 && before == k;
+      const bool on = last && after == k;
+      TG* g = grad + (int64_t)k * a.ldg + col0 + mine;
+      float* part = a.part + (2 * c + (from ? 0 : 1)) * a.dim + col0 + mine;
+      if (kVec) {
         if (!from && !on) {
-          put_row<TG, kV>(grad + (int64_t)k[j] * a.ldg + col + g * span, s[g], a.scale,
-                          a.accumulate != 0);
+          put_row<TG, kV>(g, s, a.scale, a.accumulate != 0);
         } else {
           Pack<float, kV> o;
 #pragma unroll
-          for (int e = 0; e < kV; ++e) o.v[e] = s[g][e];
-          *reinterpret_cast<Pack<float, kV>*>(a.part + (2 * c + (from ? 0 : 1)) * a.dim + col +
-                                              g * span) = o;
+          for (int e = 0; e < kV; ++e) o.v[e] = s[e];
+          *reinterpret_cast<Pack<float, kV>*>(part) = o;
         }
+      } else {
 #pragma unroll
-        for (int e = 0; e < kV; ++e) s[g][e] = 0.0f;
+        for (int e = 0; e < kV; ++e) {
+          if (mine + e * step >= width) break;
+          if (!from && !on)
+            put_row<TG, 1>(g + e * step, s + e, a.scale, a.accumulate != 0);
+          else
+            part[e * step] = s[e];
+        }
       }
-      if (on && !from && slab == 0 && threadIdx.x == 0) {
-        // a run that goes on: chunks c+1 .. end-1 start with it
-        int64_t lo = c + 1, step = 1;
-        while (lo + step < a.chunks && a.key[(lo + step) * a.chunk] == k[j]) {
-          lo += step;
-          step *= 2;
-        }
-        int64_t hi = lo + step < a.chunks ? lo + step : a.chunks;
-        while (hi - lo > 1) {
-          const int64_t mid = (lo + hi) / 2;
-          if (a.key[mid * a.chunk] == k[j]) lo = mid; else hi = mid;
-        }
+#pragma unroll
+      for (int e = 0; e < kV; ++e) s[e] = 0.0f;
+      if (on && !from && slab == 0 && x == 0) {
+        // a run that goes on: chunks c+1 .. end-1 start with it.  The end if it is near
+        // (the probes are independent), else 0.
+        constexpr int kNear = 8;
+        uint32_t probe[kNear];
+#pragma unroll
+        for (int p = 0; p < kNear; ++p)
+          probe[p] = c + 2 + p < a.chunks ? a.key[(c + 2 + p) * a.chunk] : 0xffffffffu;
+        int64_t far = 0;
+#pragma unroll
+        for (int p = kNear - 1; p >= 0; --p)
+          if (probe[p] != k) far = c + 2 + p;
         const uint32_t at = atomicAdd(&a.owner[0], 1u);
         a.owner[2 + 2 * at] = (uint32_t)c;
-        a.owner[3 + 2 * at] = (uint32_t)(lo + 1);
+        a.owner[3 + 2 * at] = (uint32_t)far;
       }
-      start = i + j + 1;
+      start = i + 1;
     }
+    __syncthreads();  // before the next copies into this buffer
   }
 }
 
 // Runs that cross chunk borders: the last partial of the chunk that the run starts in,
-// then the first partials of the chunks it goes on into, ascending.  A block joins 256
-// columns of one run: four groups of 64 threads each add every fourth chunk in order, and
-// the four sums are added in a fixed order.  A thread's four columns are consecutive, or
-// 64 apart where rows do not start on 16-byte boundaries.
+// then the first partials of the chunks it goes on into, ascending.  A block joins up to
+// 4 * tx columns of one run (tx: up to 64 threads side by side): q = 256 / tx groups of
+// threads each add every q-th chunk in order, and their sums are added in order.  A
+// thread's four columns are consecutive, or tx apart where rows do not start on 16-byte
+// boundaries.
+constexpr int kJoinThreads = 256;
 template <class TG, bool kVec>
-__global__ void __launch_bounds__(256) grad_join_kernel(GradArgs a, TG* grad) {
-  __shared__ float4 red[4][64];
+__global__ void __launch_bounds__(kJoinThreads) grad_join_kernel(GradArgs a, int tx, TG* grad) {
+  __shared__ float4 red[kJoinThreads];
   wait_prior_grid();
   allow_next_grid();
   const int64_t n = a.owner[0];
-  const int64_t slabs = (a.dim + 255) / 256;
-  const int x = threadIdx.x & 63, q = threadIdx.x >> 6;
+  const int64_t slabs = (a.dim + 4 * tx - 1) / (4 * tx);
+  const int x = threadIdx.x % tx, q = threadIdx.x / tx, nq = kJoinThreads / tx;
   for (int64_t it = blockIdx.x; it < n * slabs; it += gridDim.x) {
-    const int64_t c = a.owner[2 + 2 * (it / slabs)], end = a.owner[3 + 2 * (it / slabs)];
-    const int64_t col = it % slabs * 256 + (kVec ? 4 * x : x);
+    const int64_t c = a.owner[2 + 2 * (it / slabs)];
+    int64_t end = a.owner[3 + 2 * (it / slabs)];
+    const uint32_t k = a.key[(c + 1) * a.chunk];
+    if (end == 0) {  // a long run: the block's threads probe evenly spaced chunks together
+      int64_t lo = c + 1, hi = a.chunks;  // lo starts with the run, hi (if any) does not
+      while (hi - lo > 1) {
+        const int64_t step = (hi - lo + kJoinThreads - 1) / kJoinThreads;
+        const int64_t at = lo + (threadIdx.x + 1) * step;
+        const int same = __syncthreads_count(at < hi && a.key[at * a.chunk] == k);
+        lo += same * step;
+        hi = lo + step < hi ? lo + step : hi;
+      }
+      end = lo + 1;
+    }
+    const int64_t col = it % slabs * 4 * tx + (kVec ? 4 * x : x);
     const int64_t left = a.dim - col;
     float s[4] = {};
     if (left > 0) {
-      // every fourth partial, the first of group 0 being the start chunk's last run
+      // every q-th partial, the first of group 0 being the start chunk's last run
       const float* p0 = a.part + (2 * c + 1) * a.dim + col;
       const float* p = a.part + 2 * c * a.dim + col;
 #pragma unroll 4
-      for (int64_t j = q; j < end - c; j += 4) {
+      for (int64_t j = q; j < end - c; j += nq) {
         const float* src = j == 0 ? p0 : p + 2 * j * a.dim;
         if (kVec) {
           const float4 v = *reinterpret_cast<const float4*>(src);
@@ -576,23 +674,29 @@ __global__ void __launch_bounds__(256) grad_join_kernel(GradArgs a, TG* grad) {
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (64 * e < left) s[e] += src[64 * e];
+            if (tx * e < left) s[e] += src[tx * e];
         }
       }
     }
-    red[q][x] = make_float4(s[0], s[1], s[2], s[3]);
+    red[threadIdx.x] = make_float4(s[0], s[1], s[2], s[3]);
     __syncthreads();
     if (q == 0 && left > 0) {
-      const float4 r0 = red[0][x], r1 = red[1][x], r2 = red[2][x], r3 = red[3][x];
-      const float t[4] = {(r0.x + r1.x) + (r2.x + r3.x), (r0.y + r1.y) + (r2.y + r3.y),
-                          (r0.z + r1.z) + (r2.z + r3.z), (r0.w + r1.w) + (r2.w + r3.w)};
-      TG* dst = grad + (int64_t)a.key[(c + 1) * a.chunk] * a.ldg + col;
+      float t[4] = {};
+      const int parts = (int)(end - c < nq ? end - c : nq);
+      for (int r = 0; r < parts; ++r) {
+        const float4 v = red[r * tx + x];
+        t[0] += v.x;
+        t[1] += v.y;
+        t[2] += v.z;
+        t[3] += v.w;
+      }
+      TG* dst = grad + (int64_t)k * a.ldg + col;
       if (kVec) {
         put_row<TG, 4>(dst, t, a.scale, a.accumulate != 0);
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (64 * e < left) put_row<TG, 1>(dst + 64 * e, t + e, a.scale, a.accumulate != 0);
+          if (tx * e < left) put_row<TG, 1>(dst + tx * e, t + e, a.scale, a.accumulate != 0);
       }
     }
     __syncthreads();
@@ -612,30 +716,43 @@ cudaError_t launch(Ctx& c, int64_t grid, dim3 block, void (*fn)(P...), A... args
 }
 
 template <class TD, class TG>
-cudaError_t sum_typed(const Mat& d, const Mat& g, const GradArgs& a, Ctx& c) {
+cudaError_t sum_typed(const Mat& d, const Mat& g, const GradArgs& a, Ctrl* ctrl, Ctx& c) {
   constexpr int kV = 16 / sizeof(TD);
   const bool vec = rows_aligned(d, 16) && rows_aligned(g, kV * sizeof(TG));
-  const int v = vec ? kV : 8;  // columns per thread
-  const int64_t groups = (a.dim + v - 1) / v;
-  unsigned tx = 8;
-  while (tx < 128 && tx < groups) tx *= 2;
-  const unsigned ty = 128 / tx;
+  const int64_t groups = (a.dim + kV - 1) / kV;
+  unsigned tx = kMinTx;
+  while (tx < kSumThreads && tx < groups) tx *= 2;
+  const unsigned ty = kSumThreads / tx;
   const int64_t slabs = (groups + tx - 1) / tx;
-  const cudaError_t e = launch(c, (a.chunks + ty - 1) / ty * slabs, dim3(tx, ty),
-                               vec ? grad_sum_kernel<TD, TG, kV, 1> : grad_sum_kernel<TD, TG, 1, 8>,
-                               a, (const TD*)d.p, (TG*)g.p);
+  const auto fn = vec ? grad_sum_kernel<TD, TG, true> : grad_sum_kernel<TD, TG, false>;
+  const int smem = (a.chunk > kBatch ? 2 : 1) * (int)ty * kBatch * slab_pitch((int)tx);
+  cudaError_t e = cudaSuccess;
+  if (smem > 32768)  // (8 KB more are static)
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3((unsigned)((a.chunks + ty - 1) / ty * slabs));
+  cfg.blockDim = dim3(tx, ty);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = c.stream;
+  add_pdl_attr(c, cfg, attr);
+  ++c.launches;
+  e = cudaLaunchKernelEx(&cfg, fn, a, (const TD*)d.p, (TG*)g.p, ctrl);
   if (e != cudaSuccess || a.chunks < 2) return e;
+  int jx = 4;
+  while (jx < 64 && jx * 4 < a.dim) jx *= 2;
   // at most one run per chunk crosses into it
-  const int64_t joins = (a.chunks - 1) * ((a.dim + 255) / 256);
-  return launch(c, joins < 6 * c.num_sms ? joins : 6 * c.num_sms, dim3(256),
-                vec ? grad_join_kernel<TG, true> : grad_join_kernel<TG, false>, a, (TG*)g.p);
+  const int64_t joins = (a.chunks - 1) * ((a.dim + 4 * jx - 1) / (4 * jx));
+  return launch(c, joins < 6 * c.num_sms ? joins : 6 * c.num_sms, dim3(kJoinThreads),
+                vec ? grad_join_kernel<TG, true> : grad_join_kernel<TG, false>, a, jx, (TG*)g.p);
 }
 
 template <class TD>
-cudaError_t sum_from(const Mat& d, const Mat& g, const GradArgs& a, Ctx& c) {
-  if (g.dtype == CASGD_F32) return sum_typed<TD, float>(d, g, a, c);
-  if (g.dtype == CASGD_BF16) return sum_typed<TD, __nv_bfloat16>(d, g, a, c);
-  return sum_typed<TD, __half>(d, g, a, c);
+cudaError_t sum_from(const Mat& d, const Mat& g, const GradArgs& a, Ctrl* ctrl, Ctx& c) {
+  if (g.dtype == CASGD_F32) return sum_typed<TD, float>(d, g, a, ctrl, c);
+  if (g.dtype == CASGD_BF16) return sum_typed<TD, __nv_bfloat16>(d, g, a, ctrl, c);
+  return sum_typed<TD, __half>(d, g, a, ctrl, c);
 }
 
 // The sort (and the clearing, unless the gradient is added to) into a.key / a.pos of the
@@ -710,9 +827,9 @@ cudaError_t launch_embed_grad(const Mat& d, Ids ids, float scale, int64_t pad, b
   const GradArgs a{s.key[last], s.pos[last], s.owner, reinterpret_cast<float*>(base + L.off_part),
                    d.rows, g.rows, d.cols, d.ld, g.ld, L.chunk, L.chunks, scale,
                    accumulate ? 1 : 0};
-  if (d.dtype == CASGD_F32) return sum_from<float>(d, g, a, c);
-  if (d.dtype == CASGD_BF16) return sum_from<__nv_bfloat16>(d, g, a, c);
-  return sum_from<__half>(d, g, a, c);
+  if (d.dtype == CASGD_F32) return sum_from<float>(d, g, a, static_cast<Ctrl*>(ws), c);
+  if (d.dtype == CASGD_BF16) return sum_from<__nv_bfloat16>(d, g, a, static_cast<Ctrl*>(ws), c);
+  return sum_from<__half>(d, g, a, static_cast<Ctrl*>(ws), c);
 }
 
 }  // namespace casgd
