@@ -6,10 +6,11 @@ namespace casgd {
 namespace {
 
 constexpr int64_t kMax31 = int64_t(1) << 31;
+constexpr int64_t kMaxCols = int64_t(1) << 30;  // (column numbers plus a tile stay in 32 bits)
 
 bool check_matrix(const casgd_matrix_t* m) {
   if (!m || m->dtype < CASGD_F32 || m->dtype > CASGD_F16) return false;
-  if (m->rows < 0 || m->rows >= kMax31 || m->cols < 1 || m->cols >= kMax31) return false;
+  if (m->rows < 0 || m->rows >= kMax31 || m->cols < 1 || m->cols >= kMaxCols) return false;
   if (m->ld < m->cols || m->ld >= kMax31) return false;
   if (!m->data && m->rows > 0) return false;
   return reinterpret_cast<uintptr_t>(m->data) % elem_bytes(m->dtype) == 0;
@@ -48,7 +49,7 @@ bool check_group(const casgd_group_t* g) {
   if (!g || (g->dtype != CASGD_BF16 && g->dtype != CASGD_F16)) return false;
   if (g->rows < 0 || g->rows >= kMax31 || g->groups < 1 || g->groups > CASGD_MAX_GROUPS)
     return false;
-  if (g->k < 1 || g->n < 1 || g->k >= kMax31 || g->n >= kMax31) return false;
+  if (g->k < 1 || g->n < 1 || g->k >= kMaxCols || g->n >= kMaxCols) return false;
   if (g->ldx < g->k || g->ldw < g->k || g->ldy < g->n) return false;
   if (g->ldx >= kMax31 || g->ldw >= kMax31 || g->ldy >= kMax31) return false;
   return g->groups == 1 || (g->stride_w >= (g->n - 1) * g->ldw + g->k &&
@@ -93,7 +94,7 @@ extern "C" {
 
 int casgd_embed_workspace_size(int64_t rows, int64_t vocab, int64_t dim, size_t* bytes) {
   if (!bytes || rows < 0 || vocab < 1 || dim < 1 || rows >= kMax31 || vocab >= kMax31 ||
-      dim >= kMax31)
+      dim >= kMaxCols)
     return CASGD_ERR_ARG;
   *bytes = embed_workspace_bytes(rows, vocab, dim);
   return CASGD_OK;

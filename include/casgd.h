@@ -451,8 +451,9 @@ int casgd_chain_trace(const casgd_data_t* data, const casgd_params_t* params, vo
  *
  * Every call takes a workspace: 256-byte aligned, of the size its *_workspace_size call
  * gives, initialised once with casgd_workspace_init, owned by the caller and used by one
- * stream at a time.  Calls are asynchronous; CASGD_ERR_BAD_INDEX found on the device is
- * sticky in the workspace (casgd_get_status).  Nothing outside the given arrays is read
+ * stream at a time.  Calls are asynchronous; CASGD_ERR_BAD_INDEX found on the device (and
+ * CASGD_ERR_TIMEOUT, should a copy not arrive within a second) is sticky in the workspace
+ * (casgd_get_status).  Nothing outside the given arrays is read
  * or written whatever the token numbers and offsets hold.  Sums are FP32 or wider in a
  * fixed order (the same call on the same inputs gives the same bits), rounded once to
  * the output's type.  Inputs and outputs must not overlap except where stated.
@@ -462,7 +463,8 @@ int casgd_chain_trace(const casgd_data_t* data, const casgd_params_t* params, vo
 enum { CASGD_F32 = 0, CASGD_BF16 = 1, CASGD_F16 = 2 };
 
 /* Row-major device matrix; data aligned to its element; ld >= cols elements from row to
- * row.  Rows that start on 16-byte boundaries are read and written faster. */
+ * row; rows < 2^31, 1 <= cols < 2^30.  Rows that start on 16-byte boundaries are read and
+ * written faster. */
 typedef struct {
   void* data;
   int64_t rows, cols, ld;
@@ -477,7 +479,7 @@ typedef struct {
 } casgd_tokens_t;
 
 /* Bytes of workspace casgd_embed and casgd_embed_grad need for `rows` tokens and a
- * vocab x dim table.  rows, vocab, dim < 2^31.  Host only. */
+ * vocab x dim table.  rows, vocab < 2^31, dim < 2^30.  Host only. */
 int casgd_embed_workspace_size(int64_t rows, int64_t vocab, int64_t dim, size_t* bytes);
 
 /* Embedding lookup: out[i] = scale * table[tokens[i]], one FP32 product per element
@@ -503,7 +505,8 @@ int casgd_embed_grad(const casgd_matrix_t* dout, const casgd_tokens_t* tokens, f
  * most `rows`; anything else is held inside [0, rows] and sets CASGD_ERR_BAD_INDEX).  An
  * expert may have no rows.  16-bit inputs and outputs of one type, FP32 accumulation. */
 typedef struct {
-  int64_t rows, groups, k, n;
+  int64_t rows, groups;    /* rows < 2^31; 1 to CASGD_MAX_GROUPS experts */
+  int64_t k, n;            /* 1 <= k, n < 2^30 */
   int32_t dtype;           /* CASGD_BF16 or CASGD_F16 */
   const int32_t* offsets;
   void* x;                 /* rows x k, ldx elements from row to row */

@@ -280,6 +280,24 @@ def test_group_pitches(gpu_lib, pads):
     assert (wbuf[:, n:] == 7.0).all() and (wbuf[:, :, k:] == 7.0).all()
 
 
+def test_group_long_offsets(gpu_lib):
+    """Element offsets past 2^31 in the weights, read and written."""
+    e, n, k = 40, 8192, 8192
+    w = torch.zeros(e, n, k, device="cuda", dtype=torch.bfloat16)
+    w[39] = 0.5
+    x = torch.ones(40, k, device="cuda", dtype=torch.bfloat16)
+    y = torch.empty(40, n, device="cuda", dtype=torch.bfloat16)
+    off = offsets_of([1] * 40)
+    ws = gpu_lib.group_workspace(x, w, y)
+    gpu_lib.group_product(x, w, off, y, ws)
+    assert (y[:39] == 0).all() and (y[39] == k / 2).all()
+    y.fill_(2)
+    gpu_lib.group_product_dw(y, x, off, w, ws)
+    assert (w[39] == 2).all() and (w[0] == 2).all()
+    gpu_lib.group_product_dx(y, w, off, x, ws)
+    assert (x == 4 * n).all()
+
+
 def test_group_infinities_stay_in_their_rows(gpu_lib):
     """Inf and NaN in one expert's rows, or in rows of no expert, reach no other result."""
     counts = [37, 21, 0, 50]
@@ -693,6 +711,32 @@ def test_policy_alignment_and_in_place(gpu_lib, dt, vocab, pad, shift):
     assert outside_untouched(grad, gbuf)
     run_policy(gpu_lib, i, x, kl=0.1, clip_low=0.2, clip_high=0.3)
     assert torch.equal(x, grad) and outside_untouched(x, xbuf)
+
+
+def test_losses_long_offsets(gpu_lib):
+    """Element offsets past 2^31 in the logits and the gradient: the last rows are those of
+    a small call on them alone."""
+    rows, vocab, few = 16500, 131072, 6
+    i = policy_inputs(few, vocab, "bf16", seed=2, masked=0.0)
+    x = torch.zeros(rows, vocab, device="cuda", dtype=torch.bfloat16)
+    x[-few:] = i["x"]
+    big = {"x": x, "t": torch.full((rows,), -1, device="cuda")}
+    big["t"][-few:] = i["t"]
+    for key in ("old", "ref", "adv", "w"):
+        big[key] = torch.zeros(rows, device="cuda")
+        big[key][-few:] = i[key]
+    small = torch.empty_like(i["x"])
+    a, _ = run_policy(gpu_lib, i, small, kl=0.1)
+    b, _ = run_policy(gpu_lib, big, x, kl=0.1)                           # in place
+    assert torch.equal(b.logp[-few:], a.logp) and torch.equal(b.stats, a.stats)
+    assert torch.equal(x[-few:], small) and not x[:-few].any()
+    x[-few:] = i["x"]
+    off, ref = offsets_of([rows - few, few // 2, few - few // 2, 0]), torch.zeros(4, device="cuda")
+    off_small = offsets_of([0, few // 2, few - few // 2, 0])
+    c, _ = run_pref(gpu_lib, i["x"], i["t"], off_small, ref, small)
+    d, _ = run_pref(gpu_lib, x, big["t"], off, ref, x)
+    assert torch.equal(c.logp, d.logp) and torch.equal(c.loss, d.loss)
+    assert torch.equal(x[-few:], small) and not x[:-few].any()
 
 
 def test_policy_rows_of_weight_zero(gpu_lib):

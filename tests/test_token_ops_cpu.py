@@ -26,7 +26,7 @@ def tok(count=4, wide=1, data=FAKE):
 
 
 BAD_MATRICES = [mat(cols=0), mat(rows=-1), mat(ld=7), mat(dtype=3), mat(dtype=-1),
-                mat(data=None), mat(data=FAKE + 1), mat(rows=1 << 31), mat(ld=1 << 31)]
+                mat(data=None), mat(data=FAKE + 1), mat(rows=1 << 31), mat(ld=1 << 31), mat(cols=1 << 30)]
 
 
 def test_sizes(lib):
@@ -37,7 +37,7 @@ def test_sizes(lib):
     assert lib.casgd_preference_workspace_size(10, 1, C.byref(n)) == 0 and n.value % 256 == 0
     assert lib.casgd_policy_workspace_size(0, C.byref(n)) == 0 and n.value >= 256
     for call, args in (("embed", (-1, 5, 5)), ("embed", (5, 0, 5)), ("embed", (5, 5, 0)),
-                       ("embed", (5, 1 << 31, 5)), ("preference", (5, 0)),
+                       ("embed", (5, 1 << 31, 5)), ("embed", (5, 5, 1 << 30)), ("preference", (5, 0)),
                        ("preference", (-1, 1)), ("policy", (-1,)), ("policy", (1 << 31,))):
         fn = getattr(lib, f"casgd_{call}_workspace_size")
         assert fn(*args, C.byref(n)) == nat.CASGD_ERR_ARG
@@ -76,7 +76,8 @@ def test_group_refusals(lib):
     n = C.c_size_t(0)
     assert lib.casgd_group_workspace_size(C.byref(group()), C.byref(n)) == 0 and n.value > 0
     bad = [dict(rows=-1), dict(rows=1 << 31), dict(groups=0), dict(groups=1025), dict(k=0),
-           dict(n=0), dict(dtype=nat.CASGD_F32), dict(dtype=5), dict(ldx=7), dict(ldw=7),
+           dict(n=0), dict(k=1 << 30, ldx=1 << 30, ldw=1 << 30, stride_w=1 << 35),
+           dict(dtype=nat.CASGD_F32), dict(dtype=5), dict(ldx=7), dict(ldw=7),
            dict(ldy=23), dict(stride_w=191)]
     for b in bad:
         g = group(**b)
