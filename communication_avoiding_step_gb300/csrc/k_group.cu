@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(kThreads<kDir>, 1)
       if (!c.zero()) {
         tile::fence_before();
         __syncwarp();
-        if (lane == 0) tile::arrive_cluster(tile::peer_addr(&sh->tempty[acc], 0));
+        if (lane == 0) tile::arrive_cluster_unordered(tile::peer_addr(&sh->tempty[acc], 0));
       }
     }
   } else if (kDir == GROUP_DW) {

@@ -58,6 +58,13 @@ __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
                : "memory");
 }
+// The same without ordering this thread's memory accesses for the other CTA: for handing
+// back tensor memory, whose reads the tcgen05 fence orders.  (The release above waits for
+// every global store before it to reach L2.)
+__device__ __forceinline__ void arrive_cluster_unordered(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+               : "memory");
+}
 // mbar_try_wait that also acquires what other CTAs of the cluster released
 __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
