@@ -443,75 +443,90 @@ __global__ void __launch_bounds__(kThreads<kDir>, 1)
         }
     }
   } else if (warp == 1) {
-    if (lane == 0 && leader) {
+    if (leader) {
+      // The whole warp runs the loops, so that their values are uniform, and one lane
+      // issues the MMAs.
       constexpr bool kBf16 = !__is_same(T, __half);
       constexpr uint32_t kMStep = kDir == GROUP_Y ? 2 : 128;  // 16 of the depth, >> 4
       constexpr uint32_t kNStep = kDir == GROUP_DW ? 128 : 2;
       const uint32_t s0 = smem_u32(smem);
       const uint64_t md = tile::smem_desc(s0, kDir == GROUP_Y ? 16 : 8192, 1024);
       const uint64_t nd = tile::smem_desc(s0 + kHalf, kDir == GROUP_DW ? 8192 : 16, 1024);
+      const bool one = tile::elect_one();
+      auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, wait_on(bar, parity, sh, a.ctrl)) != 0;
+      };
       int stage = 0, iter = 0;
       uint32_t phase = 0, tphase[2] = {0, 0}, tails = 0;
       bool ok = true, any = false;
+      Tile next = pair < tiles ? tile_at<kDir>(a, sh, pair) : Tile{};
       for (int t = pair; t < tiles && ok; t += pairs) {
-        const Tile c = tile_at<kDir>(a, sh, t);
-        if (c.zero()) continue;
+        const Tile c = next;
+        if (c.zero()) {
+          next = t + pairs < tiles ? tile_at<kDir>(a, sh, t + pairs) : Tile{};
+          continue;
+        }
         const uint32_t idesc =
             tile::instr_desc(BM, c.n, kBf16, kDir != GROUP_Y, kDir == GROUP_DW);
         const int acc = iter++ & 1;
-        if (!(ok = wait_on(&sh->tempty[acc], tphase[acc] ^ 1u, sh, a.ctrl))) break;
+        if (!(ok = wait_warp(&sh->tempty[acc], tphase[acc] ^ 1u))) break;
         tphase[acc] ^= 1u;
         tile::fence_after();
         const uint32_t d = tmem + (uint32_t)(acc * BN);
-        uint32_t accumulate = 0;
-        auto step = [&](int s) {
-          tile::mma_pair(d, md + (uint64_t)(stage * (kStageBytes >> 4) + s * kMStep),
-                         nd + (uint64_t)(stage * (kStageBytes >> 4) + s * kNStep), idesc,
-                         accumulate);
-          accumulate = 1;
-        };
-        auto next_stage = [&] {
-          tile::commit_pair(&sh->empty[stage], 0x3);
+        any = true;
+        // `steps` steps of 16 of the slice in the next stage
+        auto slice = [&](int steps, bool first) {
+          if (!(ok = wait_warp(&sh->full[stage], phase))) return;
+          tile::fence_after();
+          const uint64_t m = md + (uint64_t)(stage * (kStageBytes >> 4));
+          const uint64_t n = nd + (uint64_t)(stage * (kStageBytes >> 4));
+          if (one) {
+            if (steps == BK / 16) {
+#pragma unroll
+              for (int s = 0; s < BK / 16; ++s)
+                tile::mma_pair(d, m + s * kMStep, n + s * kNStep, idesc, first && s == 0 ? 0u : 1u);
+            } else {
+#pragma unroll 1
+              for (int s = 0; s < steps; ++s)
+                tile::mma_pair(d, m + s * kMStep, n + s * kNStep, idesc, first && s == 0 ? 0u : 1u);
+            }
+            tile::commit_pair(&sh->empty[stage], 0x3);
+          }
           if (++stage == kSt) {
             stage = 0;
             phase ^= 1u;
           }
         };
-        any = true;
-        // whole slices unrolled (as a loop of its own: issued a third faster)
-        for (int kb = 0; kb < c.depth / BK; ++kb) {
-          if (!(ok = wait_on(&sh->full[stage], phase, sh, a.ctrl))) break;
-          tile::fence_after();
-#pragma unroll
-          for (int s = 0; s < BK / 16; ++s) step(s);
-          next_stage();
-        }
-        if (ok && c.depth % BK != 0 && (ok = wait_on(&sh->full[stage], phase, sh, a.ctrl))) {
-          tile::fence_after();
-#pragma unroll 1
-          for (int s = 0; s < (c.depth % BK + 15) / 16; ++s) step(s);
-          next_stage();
-        }
+        const int whole = c.depth / BK, rest = (c.depth % BK + 15) / 16;
+        for (int kb = 0; kb + 1 < whole && ok; ++kb) slice(BK / 16, kb == 0);
+        // the next tile is looked up while MMAs are queued, before the last whole slice
+        next = t + pairs < tiles ? tile_at<kDir>(a, sh, t + pairs) : Tile{};
+        if (whole > 0 && ok) slice(BK / 16, whole == 1);
+        if (rest > 0 && ok) slice(rest, whole == 0);
         if (kDir == GROUP_DW && ok && c.last) {
           const int b = tails % kTails;
-          if ((ok = wait_on<WAIT_CLUSTER>(&sh->mended[b], tails / kTails & 1u, sh, a.ctrl))) {
+          ok = __all_sync(0xffffffffu, wait_on<WAIT_CLUSTER>(&sh->mended[b], tails / kTails & 1u,
+                                                             sh, a.ctrl)) != 0;
+          if (ok && one) {
             tile::fence_after();
             const uint32_t sm = smem_u32(tail_buf + b * kTailBytes);
             tile::mma_pair(d, tile::smem_desc(sm, 2048, 1024),
-                           tile::smem_desc(sm + kTailBytes / 2, 2048, 1024), idesc, accumulate);
+                           tile::smem_desc(sm + kTailBytes / 2, 2048, 1024), idesc,
+                           c.depth > 0 ? 1u : 0u);
             tile::commit_pair(&sh->used[b], 0x3);
-            ++tails;
           }
+          ++tails;
         }
         if (!ok) break;
-        tile::commit_pair(&sh->tfull[acc], 0x3);
+        if (one) tile::commit_pair(&sh->tfull[acc], 0x3);
       }
-      if (any) {  // every MMA has completed before the pair frees TMEM
+      if (any && one) {  // every MMA has completed before the pair frees TMEM
         tile::commit_pair(&sh->drain, 0x1);
         const uint64_t t0 = globaltimer_ns();
         while (!mbar_try_wait(&sh->drain, 0) && globaltimer_ns() - t0 < kTimeoutNs) {
         }
       }
+      __syncwarp();
     }
   } else if (warp < 2 + kEpiWarps) {
     const int quarter = warp & 3;  // TMEM lanes 32 * quarter .. + 31
