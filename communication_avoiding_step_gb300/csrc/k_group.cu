@@ -382,39 +382,41 @@ __global__ void __launch_bounds__(kThreads<kDir>, 1)
   const uint32_t tmem = sh->tmem_base;
   const int tiles = sh->tiles;
   if (warp == 0) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, issued = 0, last_par = 0;
-      bool ok = true;
-      for (int t = pair; t < tiles && ok; t += pairs) {
-        const Tile c = tile_at<kDir>(a, sh, t);
-        const int half = c.n / 2;  // this CTA's part of the N side
-        const int boxes64 = (half + 63) / 64;
-        const int box = half <= 16 ? 0 : (half + 31) / 32;  // 16, 32, 64, 96 or 128 rows
-        const uint32_t bytes =
-            kHalf + (kDir == GROUP_DW ? boxes64 * 8192u : box ? box * 4096u : 2048u);
-        const int m = c.m0 + rank * 128;
-        for (int kb = 0; kb < c.nkb; ++kb) {
-          if (!wait_on(&sh->empty[stage], phase ^ 1u, sh, a.ctrl)) {
-            ok = false;
-            break;
-          }
-          const uint32_t sm = smem_u32(smem + (size_t)stage * kStageBytes), sn = sm + kHalf;
-          const uint32_t bar = tile::peer_addr(&sh->full[stage], 0);
+    // (the whole warp, as below)
+    const bool one = tile::elect_one();
+    const uint32_t s0 = smem_u32(smem);
+    int stage = 0;
+    uint32_t phase = 0, issued = 0, last_par = 0;
+    bool ok = true;
+    Tile next = pair < tiles ? tile_at<kDir>(a, sh, pair) : Tile{};
+    for (int t = pair; t < tiles && ok; t += pairs) {
+      const Tile c = next;
+      const int half = c.n / 2;  // this CTA's part of the N side
+      const int boxes64 = (half + 63) / 64;
+      const int box = half <= 16 ? 0 : (half + 31) / 32;  // 16, 32, 64, 96 or 128 rows
+      const uint32_t bytes =
+          kHalf + (kDir == GROUP_DW ? boxes64 * 8192u : box ? box * 4096u : 2048u);
+      const int m = c.m0 + rank * 128, k = c.n0 + rank * half;
+      const int row = kDir == GROUP_DW ? c.row0 : c.row0 + k;
+      for (int kb = 0; kb < c.nkb; ++kb) {
+        ok = __all_sync(0xffffffffu, wait_on(&sh->empty[stage], phase ^ 1u, sh, a.ctrl)) != 0;
+        if (!ok) break;
+        const uint32_t sm = s0 + (uint32_t)stage * kStageBytes, sn = sm + kHalf;
+        const uint32_t bar = tile::peer_addr(&sh->full[stage], 0);
+        const int d = kb * BK;
+        if (one) {
           if (leader) mbar_expect_tx(&sh->full[stage], 2 * bytes);
-          const int d = kb * BK;
           if (kDir == GROUP_DW) {
             if (a.blocks_m)
-              tile::tma_load_3d(sm, &maps.m, bar, 0, c.row0 + d, m / 64);
+              tile::tma_load_3d(sm, &maps.m, bar, 0, row + d, m / 64);
             else
               for (int i = 0; i < 2; ++i)
-                tile::tma_load_2d(sm + i * 8192, &maps.m, bar, m + i * 64, c.row0 + d);
-            const int k = c.n0 + rank * half;
+                tile::tma_load_2d(sm + i * 8192, &maps.m, bar, m + i * 64, row + d);
             if (a.blocks_n && half == 128)
-              tile::tma_load_3d(sn, &maps.n[1], bar, 0, c.row0 + d, k / 64);
+              tile::tma_load_3d(sn, &maps.n[1], bar, 0, row + d, k / 64);
             else
               for (int i = 0; i < boxes64; ++i)
-                tile::tma_load_2d(sn + i * 8192, &maps.n[0], bar, k + i * 64, c.row0 + d);
+                tile::tma_load_2d(sn + i * 8192, &maps.n[0], bar, k + i * 64, row + d);
           } else {
             if (kDir == GROUP_Y)
               tile::tma_load_3d(sm, &maps.m, bar, d, m, c.e);
@@ -423,25 +425,27 @@ __global__ void __launch_bounds__(kThreads<kDir>, 1)
             else
               for (int i = 0; i < 2; ++i)
                 tile::tma_load_3d(sm + i * 8192, &maps.m, bar, m + i * 64, d, c.e);
-            tile::tma_load_2d(sn, &maps.n[box], bar, d, c.row0 + c.n0 + rank * half);
+            tile::tma_load_2d(sn, &maps.n[box], bar, d, row);
           }
-          issued |= 1u << stage;
-          last_par = (last_par & ~(1u << stage)) | (phase << stage);
-          if (++stage == kSt) {
-            stage = 0;
-            phase ^= 1u;
-          }
+        }
+        issued |= 1u << stage;
+        last_par = (last_par & ~(1u << stage)) | (phase << stage);
+        if (++stage == kSt) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      // every copy of the pair has landed before the CTAs may exit
-      for (int st = 0; st < kSt && leader; ++st)
-        if (issued & (1u << st)) {
-          const uint64_t t0 = globaltimer_ns();
-          while (!mbar_try_wait(&sh->full[st], (last_par >> st) & 1u) &&
-                 globaltimer_ns() - t0 < kTimeoutNs) {
-          }
-        }
+      next = t + pairs < tiles ? tile_at<kDir>(a, sh, t + pairs) : Tile{};
     }
+    // every copy of the pair has landed before the CTAs may exit
+    for (int st = 0; st < kSt && leader && one; ++st)
+      if (issued & (1u << st)) {
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(&sh->full[st], (last_par >> st) & 1u) &&
+               globaltimer_ns() - t0 < kTimeoutNs) {
+        }
+      }
+    __syncwarp();
   } else if (warp == 1) {
     if (leader) {
       // The whole warp runs the loops, so that their values are uniform, and one lane
