@@ -568,39 +568,70 @@ __global__ void __launch_bounds__(kThreads<kDir>, 1)
     }
   } else if (kDir == GROUP_DW) {
     // The last tokens: 16 of them, zeros past the group's end, in every 64-column block.
-    uint32_t tails = 0;
-    for (int t = pair; t < tiles; t += pairs) {
-      const Tile c = tile_at<kDir>(a, sh, t);
-      if (c.last == 0) continue;
-      const int b = tails % kTails, half = c.n / 2, nb = (half + 63) / 64;
-      const uint32_t par = tails / kTails & 1u;
-      uint8_t* buf = tail_buf + b * kTailBytes;
-      int ok = 1;
-      if (lane == 0) {
-        ok = wait_on<WAIT_IDLE>(&sh->used[b], par ^ 1u, sh, a.ctrl) ? 1 : 0;
-        if (ok) {
-          const uint32_t bar = tile::peer_addr(&sh->tail[b], rank), sm = smem_u32(buf);
-          const int row = c.row0 + c.depth;
+    // Copies are issued as far ahead as there are buffers, so that their latencies overlap.
+    const bool one = tile::elect_one();
+    auto find = [&](int& t) {  // the next tile, from t on, with last tokens
+      Tile c{};
+      for (; t < tiles; t += pairs) {
+        c = tile_at<kDir>(a, sh, t);
+        if (c.last) break;
+      }
+      return c;
+    };
+    int ti = pair, tm = pair;    // tiles of the next copy and of the next to mend
+    uint32_t ni = 0, nm = 0;     // their numbers
+    Tile ci = find(ti), cm = ci;
+    tm = ti;
+    bool ok = true;
+    while (tm < tiles && ok) {
+      while (ti < tiles && ni < nm + kTails) {
+        const int b = ni % kTails, half = ci.n / 2, nb = (half + 63) / 64;
+        const uint32_t par = ni / kTails & 1u;
+        bool free = __all_sync(0xffffffffu, mbar_try_wait(&sh->used[b], par ^ 1u)) != 0;
+        if (!free && ni > nm) break;  // mend what is under way first
+        if (!free)
+          free = ok = __all_sync(0xffffffffu, wait_on<WAIT_IDLE>(&sh->used[b], par ^ 1u, sh,
+                                                                 a.ctrl)) != 0;
+        if (!ok) break;
+        if (one) {
+          const uint32_t bar = tile::peer_addr(&sh->tail[b], rank);
+          const uint32_t sm = smem_u32(tail_buf + b * kTailBytes);
+          const int row = ci.row0 + ci.depth;
           mbar_expect_tx(&sh->tail[b], (uint32_t)(2 + nb) * 2048);
           for (int i = 0; i < 2; ++i)
-            tile::tma_load_2d(sm + i * 2048, &maps.n[3], bar, c.m0 + rank * 128 + i * 64, row);
+            tile::tma_load_2d(sm + i * 2048, &maps.n[3], bar, ci.m0 + rank * 128 + i * 64, row);
           for (int i = 0; i < nb; ++i)
             tile::tma_load_2d(sm + kTailBytes / 2 + i * 2048, &maps.n[2], bar,
-                              c.n0 + rank * half + i * 64, row);
-          ok = wait_on(&sh->tail[b], par, sh, a.ctrl) ? 1 : 0;
+                              ci.n0 + rank * half + i * 64, row);
         }
+        ++ni;
+        ti += pairs;
+        ci = find(ti);
       }
-      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-      __syncwarp();
-      const int zr = 16 - c.last;
+      if (!ok) break;
+      const int b = nm % kTails, nb = (cm.n / 2 + 63) / 64;
+      ok = __all_sync(0xffffffffu, wait_on(&sh->tail[b], nm / kTails & 1u, sh, a.ctrl)) != 0;
+      if (!ok) break;
+      uint8_t* buf = tail_buf + b * kTailBytes;
+      const int zr = 16 - cm.last;
       for (int i = lane; i < (2 + nb) * zr * 8; i += 32)
-        *reinterpret_cast<uint4*>(buf + i / (zr * 8) * 2048 + (c.last + i / 8 % zr) * 128 +
+        *reinterpret_cast<uint4*>(buf + i / (zr * 8) * 2048 + (cm.last + i / 8 % zr) * 128 +
                                   (i & 7) * 16) = make_uint4(0, 0, 0, 0);
       tile::fence_async_smem();
       __syncwarp();
-      if (lane == 0) tile::arrive_cluster(tile::peer_addr(&sh->mended[b], 0));
-      ++tails;
+      if (one) tile::arrive_cluster(tile::peer_addr(&sh->mended[b], 0));
+      ++nm;
+      tm += pairs;
+      cm = find(tm);
     }
+    // (after a wait that failed: copies still under way land before the CTA exits)
+    for (; nm < ni; ++nm) {
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(&sh->tail[nm % kTails], nm / kTails & 1u) &&
+             globaltimer_ns() - t0 < kTimeoutNs) {
+      }
+    }
+    __syncwarp();
   }
   tile::fence_before();
   __syncthreads();
