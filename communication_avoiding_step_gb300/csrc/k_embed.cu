@@ -144,7 +144,7 @@ struct GradLayout {
 GradLayout grad_layout(int64_t rows, int64_t vocab, int64_t dim) {
   GradLayout L;
   // One cluster, two pairs per thread as long as that keeps it within its largest size
-  // (17,102 tokens: 24 -> 18 us against eight pairs per thread on fewer CTAs).
+  // (17,102 tokens of 16 columns: 25 -> 21 us against eight pairs per thread on fewer CTAs).
   L.tiles = (rows + 2 * kSortThreads - 1) / (2 * kSortThreads);
   if (L.tiles < 1) L.tiles = 1;
   if (L.tiles > kMaxCluster) L.tiles = kMaxCluster;

@@ -16,9 +16,9 @@
 //   dW      the other dimension of the weights; the tokens are summed over.
 // Each CTA stages its 128 rows of the M side and its half of the N side, 64 deep: 32 KB for
 // 256 x 256 x 64 products, two thirds of what one CTA needs for a 128 x 256 tile of its own.
-// What bounds it: the copy engine, at about two cycles per 128-byte row, needs as long for a
-// slice as the tensor cores (512 cycles), and a ring of 192 KB per SM has to cover the
-// latency.  Measured, BF16: 8192^3 1.85 PFLOP/s (dW 1.77); 16384 rows of 32 ragged experts,
+// What bounds it: the copies into shared memory take as long as the products (8192^3: 459 us
+// alone, the products alone 484, together 593), and a ring of 192 KB per SM has to cover
+// their latency.  Measured, BF16: 8192^3 1.85 PFLOP/s (dW 1.77); 16384 rows of 32 ragged experts,
 // 2048 x 2816: Y 124 us, dX 123, dW 158 (99, 102 and 130 without the loads); one 128 x 256
 // tile per CTA took 180 (Y) and 220 us (dW).
 //

@@ -14,7 +14,7 @@
 //   on chip, so one launch reads every row for its sum, one adds up the pairs, and one
 //   reads the rows again for the gradient, in the opposite order, so that what L2 still
 //   holds comes first.
-// Measured, BF16, 128,000 columns: policy 8192 rows 765 us (5.3 TB/s of one read and one
+// Measured, BF16, 128,000 columns: policy 8192 rows 765 us (5.2 TB/s of one read and one
 // write); preference 12,288 rows 1385 us (6.4 TB/s of two reads and one write).
 // Rows wider than kWarpCols go through stream_kernel, a ring of bulk copies per block;
 // shorter ones take a warp each (warp kernels), without shared memory.
