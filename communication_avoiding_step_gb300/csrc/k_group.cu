@@ -46,6 +46,7 @@
 // TMA needs rows on 16-byte boundaries.  Inputs without them (odd widths or pitches) are
 // copied once into the workspace with padded rows; outputs without them are stored element
 // by element.
+#include <atomic>
 #include <cstring>
 
 #include "tc_tile.cuh"
@@ -112,13 +113,17 @@ struct GroupTc {
 };
 
 // Bounded wait: false (and the CTA's abort word set) if the phase does not complete in
-// time or another role of this CTA gave up.  The clock is read every kPolls tries only: it
-// takes longer than a try, and a wait that polls late holds up the ring.
+// time or another role of this CTA gave up.  Waits for a stage have a second; those for
+// work on `slices` slices have kSliceNs for each of them besides.  The clock is read every
+// kPolls tries only: it takes longer than a try, and a wait that polls late holds up the
+// ring.
 // Warps with time to spare sleep between tries, which leaves shared memory to the copies.
 constexpr uint32_t kPolls = 256;
+constexpr uint64_t kSliceNs = 8192;  // (a slice takes 270 ns from L2, about 1 us from memory)
 enum WaitKind { WAIT_HOT, WAIT_IDLE, WAIT_CLUSTER };  // (acquiring what the other CTA released)
 template <WaitKind kKind = WAIT_HOT>
-__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, Shared* sh, Ctrl* ctrl) {
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, Shared* sh, Ctrl* ctrl,
+                                        uint64_t slices = 0) {
   uint64_t t0 = 0;
   for (uint32_t n = 1;; ++n) {
     if (kKind == WAIT_CLUSTER ? tile::try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))
@@ -128,7 +133,7 @@ __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, Shared* 
       if (sh->abort) return false;
       const uint64_t now = globaltimer_ns();
       if (t0 == 0) t0 = now;
-      if (now - t0 > kTimeoutNs) {
+      if (now - t0 > kTimeoutNs + slices * kSliceNs) {
         sh->abort = 1;
         atomicOr(&ctrl->status, ST_TIMEOUT);
         return false;
@@ -551,7 +556,8 @@ __global__ void __launch_bounds__(kThreads<kDir>, 1)
       if (!c.zero()) {
         acc = iter++ & 1;
         int ok = 1;
-        if (lane == 0) ok = wait_on<WAIT_IDLE>(&sh->tfull[acc], tphase[acc], sh, a.ctrl) ? 1 : 0;
+        if (lane == 0)
+          ok = wait_on<WAIT_IDLE>(&sh->tfull[acc], tphase[acc], sh, a.ctrl, c.nkb) ? 1 : 0;
         if (!__shfl_sync(0xffffffffu, ok, 0)) break;
         tphase[acc] ^= 1u;
         tile::fence_after();
@@ -585,6 +591,8 @@ __global__ void __launch_bounds__(kThreads<kDir>, 1)
       }
       return c;
     };
+    // (between two uses of a buffer the MMAs may go through any of this pair's tiles)
+    const uint64_t slices = (uint64_t)(tiles / pairs + 1) * (uint32_t)(a.rows / BK + 1);
     int ti = pair, tm = pair;    // tiles of the next copy and of the next to mend
     uint32_t ni = 0, nm = 0;     // their numbers
     Tile ci = find(ti), cm = ci;
@@ -598,7 +606,7 @@ __global__ void __launch_bounds__(kThreads<kDir>, 1)
         if (!free && ni > nm) break;  // mend what is under way first
         if (!free)
           free = ok = __all_sync(0xffffffffu, wait_on<WAIT_IDLE>(&sh->used[b], par ^ 1u, sh,
-                                                                 a.ctrl)) != 0;
+                                                                 a.ctrl, slices)) != 0;
         if (!ok) break;
         if (one) {
           const uint32_t bar = tile::peer_addr(&sh->tail[b], rank);
@@ -672,7 +680,8 @@ typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void
                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 EncodeFn encode_fn() {
-  static EncodeFn fn = nullptr;
+  static std::atomic<EncodeFn> found{nullptr};  // (calls may come from several host threads)
+  EncodeFn fn = found.load(std::memory_order_acquire);
   if (!fn) {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -681,6 +690,7 @@ EncodeFn encode_fn() {
         q != cudaDriverEntryPointSuccess)
       return nullptr;
     fn = reinterpret_cast<EncodeFn>(p);
+    found.store(fn, std::memory_order_release);
   }
   return fn;
 }
