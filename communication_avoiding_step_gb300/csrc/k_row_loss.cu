@@ -39,25 +39,36 @@ __device__ __forceinline__ float fast_exp2(float t) {
   return r;
 }
 
-// Of the values x seen: the largest x * scale (m, rounded once) and the sum s of
-// 2^(x * scale - m), each exponent one fused multiply-add (m = -inf, s = 0: none seen).
-// scale is log2(e) over the temperature.
+// Of the values x seen: the largest (m) and the sum s of 2^((x - m) * scale) (m = -inf,
+// s = 0: none seen).  scale is log2(e) over the temperature.  An exponent is one fused
+// multiply-add, x * scale less m * scale rounded once, which every sum of the row uses
+// alike.  Where m is finite but m * scale is not (rows of a type's lowest value, very low
+// temperatures) the difference is taken first instead.
 struct MaxSum {
   float m, s;
 };
-__device__ __forceinline__ float rescale(float m, float top) {
-  return m == top ? 1.0f : fast_exp2(m - top);
+__device__ __forceinline__ bool scales_out(float m, float base) {
+  return fabsf(base) == INFINITY && fabsf(m) < INFINITY;
 }
-__device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b) {
+__device__ __forceinline__ float exponent(float x, float m, float scale) {
+  const float base = __fmul_rn(m, scale);
+  return scales_out(m, base) ? (x - m) * scale : fmaf(x, scale, -base);
+}
+__device__ __forceinline__ float rescale(float m, float top, float scale) {
+  const float b = __fmul_rn(m, scale), t = __fmul_rn(top, scale);
+  const bool out = scales_out(m, b) || scales_out(top, t);
+  return m == top ? 1.0f : fast_exp2(out ? (m - top) * scale : b - t);
+}
+__device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b, float scale) {
   const float m = fmaxf(a.m, b.m);
-  return {m, a.s * rescale(a.m, m) + b.s * rescale(b.m, m)};
+  return {m, a.s * rescale(a.m, m, scale) + b.s * rescale(b.m, m, scale)};
 }
 template <int kLanes>
-__device__ __forceinline__ MaxSum join_lanes(MaxSum r) {
+__device__ __forceinline__ MaxSum join_lanes(MaxSum r, float scale) {
   float m = r.m;
 #pragma unroll
   for (int o = kLanes / 2; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float s = r.s * rescale(r.m, m);
+  float s = r.s * rescale(r.m, m, scale);
 #pragma unroll
   for (int o = kLanes / 2; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
   return {m, s};
@@ -157,17 +168,23 @@ __device__ __forceinline__ MaxSum granules_max_sum(const Granule (&p)[kN], float
   for (int i = 1; i < 4 * kN; ++i) mw = W::max(mw, p[i / 4].w[i % 4]);
   float mf[W::kPer];
   W::get(mw, mf);
-  const float m = fmaxf(mf[0], mf[W::kPer - 1]) * scale;
-  const float base = m == -INFINITY ? 0.0f : m;
+  const float m = fmaxf(mf[0], mf[W::kPer - 1]);
+  const float b = __fmul_rn(m, scale);
   float s[4] = {};
+  auto add = [&](float off, float base) {
 #pragma unroll
-  for (int i = 0; i < 4 * kN; ++i) {
-    float f[W::kPer];
-    W::get(p[i / 4].w[i % 4], f);
+    for (int i = 0; i < 4 * kN; ++i) {
+      float f[W::kPer];
+      W::get(p[i / 4].w[i % 4], f);
 #pragma unroll
-    for (int e = 0; e < W::kPer; ++e)
-      s[(i * W::kPer + e) & 3] += fast_exp2(fmaf(f[e], scale, -base));
-  }
+      for (int e = 0; e < W::kPer; ++e)
+        s[(i * W::kPer + e) & 3] += fast_exp2(fmaf(f[e] - off, scale, -base));
+    }
+  };
+  if (__builtin_expect(scales_out(m, b), 0))
+    add(m, 0.0f);
+  else
+    add(0.0f, m == -INFINITY ? 0.0f : b);
   return {m, (s[0] + s[1]) + (s[2] + s[3])};
 }
 
@@ -219,19 +236,27 @@ __device__ __forceinline__ void put_granule(const Row<T>& r, T* out, bool aligne
   }
 }
 
-// k * 2^(x * scale - m) of a granule: with k = -g / s, its gradient away from the target.
+// k * 2^((x - m) * scale) of a granule: with k = -g / s, its gradient away from the target.
 template <class T>
 __device__ __forceinline__ Granule softmax_part(const Granule& x, float scale, float m, float k) {
   using W = Words<T>;
+  const float b = __fmul_rn(m, scale);
   Granule o;
+  auto set = [&](float off, float base) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float f[W::kPer];
-    W::get(x.w[i], f);
+    for (int i = 0; i < 4; ++i) {
+      float f[W::kPer];
+      W::get(x.w[i], f);
 #pragma unroll
-    for (int e = 0; e < W::kPer; ++e) f[e] = k * fast_exp2(fmaf(f[e], scale, -m));
-    o.w[i] = W::put(f);
-  }
+      for (int e = 0; e < W::kPer; ++e)
+        f[e] = k * fast_exp2(fmaf(f[e] - off, scale, -base));
+      o.w[i] = W::put(f);
+    }
+  };
+  if (__builtin_expect(scales_out(m, b), 0))
+    set(m, 0.0f);
+  else
+    set(0.0f, b);
   return o;
 }
 
@@ -245,24 +270,28 @@ __device__ __forceinline__ MaxSum warp_max_sum(const Row<T>& r, int lane, float 
     Granule p[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) p[u] = r.load(g + 32 * u);
-    acc = join(acc, granules_max_sum<T, kU>(p, scale));
+    acc = join(acc, granules_max_sum<T, kU>(p, scale), scale);
   }
 #pragma unroll 1
   for (; g < r.granules; g += 32) {
     const Granule p[1] = {r.load(g)};
-    acc = join(acc, granules_max_sum<T, 1>(p, scale));
+    acc = join(acc, granules_max_sum<T, 1>(p, scale), scale);
   }
-  return join_lanes<32>(acc);
+  return join_lanes<32>(acc, scale);
 }
 
-// The target's log probability.
+// The target's log probability, at most 0 (rounding may leave it above).  A finite logit
+// whose scaled distance to the maximum overflows: in natural units first.
 __device__ __forceinline__ float log_prob(float xt, MaxSum r, float scale) {
   constexpr float kLn2 = 0.6931471805599453f;
-  return fmaf(xt, scale, -r.m) * kLn2 - logf(r.s);
+  const float t = exponent(xt, r.m, scale);
+  const bool out = t == -INFINITY && xt > -INFINITY;
+  const float lp = (out ? (xt - r.m) * (scale * kLn2) : t * kLn2) - logf(r.s);
+  return lp > 0.0f ? 0.0f : lp;
 }
 // g * (1 - softmax) at the target
 __device__ __forceinline__ float target_grad(float g, float xt, MaxSum r, float scale) {
-  return g * (1.0f - fast_exp2(fmaf(xt, scale, -r.m)) / r.s);
+  return g * (1.0f - fast_exp2(exponent(xt, r.m, scale)) / r.s);
 }
 
 // Writes g * (onehot - softmax), or zeros, to a row by a warp.
@@ -480,9 +509,10 @@ __device__ __forceinline__ RowLoss policy_row(const PolicyArgs& a, const RowInfo
   if (f.weight == 0.0f) return o;
   const float ratio = expf(o.lp - f.old_logp);
   const float held = fminf(fmaxf(ratio, 1.0f - a.clip_low), 1.0f + a.clip_high);
-  const bool inside =
-      f.adv >= 0.0f ? ratio <= 1.0f + a.clip_high : ratio >= 1.0f - a.clip_low;
-  float l = -fminf(ratio * f.adv, held * f.adv), d = inside ? -ratio * f.adv : 0.0f;
+  const bool outside = f.adv >= 0.0f ? ratio > 1.0f + a.clip_high : ratio < 1.0f - a.clip_low;
+  // (minimum and maximum drop a NaN: a ratio that is one stays one)
+  float l = ratio == ratio ? -fminf(ratio * f.adv, held * f.adv) : ratio;
+  float d = outside ? 0.0f : -ratio * f.adv;
   if (a.ref_logp) {
     const float away = f.ref_logp - o.lp, em = expm1f(away);
     o.kl = f.weight * (em - away);
@@ -490,7 +520,7 @@ __device__ __forceinline__ RowLoss policy_row(const PolicyArgs& a, const RowInfo
     d -= a.kl * em;
   }
   o.loss = f.weight * l;
-  o.clipped = inside ? 0.0f : f.weight;
+  o.clipped = outside ? f.weight : 0.0f;
   o.g = a.grad_scale * d * f.weight * inv_t;
   return o;
 }
@@ -780,20 +810,20 @@ __global__ void __launch_bounds__(kStreamThreads, 2) stream_kernel(A a, W w) {
               p[u] = g + tid + u * kBlock < n ? buf[u * kBlock] : no_granule<T>();
           }
           release();
-          acc = join(acc, granules_max_sum<T, kU>(p, scale));
+          acc = join(acc, granules_max_sum<T, kU>(p, scale), scale);
         }
         if (edge >= 0) {
           const Granule p[1] = {eg};
-          acc = join(acc, granules_max_sum<T, 1>(p, scale));
+          acc = join(acc, granules_max_sum<T, 1>(p, scale), scale);
         }
-        acc = join_lanes<32>(acc);
+        acc = join_lanes<32>(acc, scale);
         if (lane == 0) sh->part[warp] = acc;
       } else if (ok) {
         release();
       }
       if (!meet_ok(ok)) break;
       if (warp == 0) {
-        if (read) r = join_lanes<kWarps>(sh->part[lane % kWarps]);
+        if (read) r = join_lanes<kWarps>(sh->part[lane % kWarps], scale);
         if constexpr (kMode == STREAM_POLICY) {
           o = policy_row(a, f, r, inv_t, scale);
           if (lane == 0) {

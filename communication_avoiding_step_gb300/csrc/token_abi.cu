@@ -1,5 +1,7 @@
 // C entry points of the token-model operators (declared in include/casgd.h): argument
 // checks, then the launchers of k_embed.cu, k_group.cu and k_row_loss.cu.
+#include <cfloat>
+
 #include "token_common.cuh"
 
 namespace casgd {
@@ -187,8 +189,10 @@ int casgd_policy_loss(const casgd_matrix_t* logits, const casgd_tokens_t* target
   if (!aligned4(weights) || !aligned4(old_logp) || !aligned4(ref_logp) || !aligned4(adv) ||
       !aligned4(logp))
     return CASGD_ERR_ARG;
+  // (and the factor of the logits, 1 / temperature, is a positive number too)
   if (!(p->kl == p->kl) || !(p->clip_low >= 0.0f) || !(p->clip_high >= 0.0f) ||
-      !(p->temperature > 0.0f) || !(p->grad_scale == p->grad_scale))
+      !(p->temperature > 0.0f && 1.0f / p->temperature > 0.0f &&
+        1.0f / p->temperature <= FLT_MAX) || !(p->grad_scale == p->grad_scale))
     return CASGD_ERR_ARG;
   int rc = check_ws(ws, ws_bytes, policy_workspace_bytes(logits->rows));
   Ctx c{};

@@ -572,7 +572,7 @@ typedef struct {
   float kl;            /* factor of the KL term                                     */
   float clip_low;      /* the ratio is held in [1 - clip_low, 1 + clip_high]        */
   float clip_high;
-  float temperature;   /* > 0: the logits are divided by it                         */
+  float temperature;   /* > 0, 1 / it finite and > 0: the logits are divided by it  */
   float grad_scale;    /* factor of the gradient (loss scaling)                     */
 } casgd_policy_t;
 

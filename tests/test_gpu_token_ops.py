@@ -807,3 +807,135 @@ def test_another_stream(gpu_lib):
                         ref_logp=i["ref"], kl=0.1, stream=torch.cuda.current_stream())
     torch.cuda.synchronize()
     assert torch.equal(grad, g2)
+
+
+# rows whose scaled logits leave FP32
+FAR_COLS = [1, 5, 2048, 2049, 33000]
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("vocab", FAR_COLS)
+def test_policy_rows_of_the_lowest_value(gpu_lib, dt, vocab):
+    """Rows (0) of the type's lowest value, a vocabulary masked whole: uniform; (1) with one
+    logit of the type's largest value, the target: certain; (2) whose target alone is
+    lowest: its log probability is that value (to rounding) and its gradient zero.  Powers
+    of two and exponentials of zero are exact, sums of ones too: what is left is the
+    logarithm (2 ulp) and its product."""
+    low, top = torch.finfo(DT[dt]).min, torch.finfo(DT[dt]).max
+    x = randn(3, vocab, seed=5).to(DT[dt])
+    x[0] = low
+    t = torch.tensor([vocab // 2, vocab - 1, 0], device="cuda")
+    x[1, vocab - 1], x[2, 0] = top, low
+    one = torch.ones(3, device="cuda")
+    logv = float(np.log(vocab))
+    i = dict(x=x, t=t, w=one.clone(), old=torch.tensor([-logv, 0.0, 0.0], device="cuda"),
+             adv=one)
+    grad = torch.full_like(x, 3.0)
+    out, ws = run_policy(gpu_lib, i, grad, ref=False)
+    assert abs(float(out.logp[0]) + logv) <= 4 * E32 * (logv + 1)
+    assert float(out.logp[1]) == 0
+    if vocab > 1:
+        lse = float(torch.logsumexp(x[2, 1:].double(), 0))
+        want = low - lse
+        assert abs(float(out.logp[2]) - want) <= 4 * E32 * abs(want) + 8 * E32 * (1 + abs(lse))
+    want = torch.full((vocab,), 1.0 / vocab, device="cuda", dtype=torch.float64)
+    want[vocab // 2] -= 1.0
+    close(grad[0], want, ULP[dt] * want.abs() + 16 * E32 * (logv + 1) * want.abs() + TINY[dt] + E32)
+    assert float(grad[1].float().abs().max()) == 0
+    if vocab > 1:
+        assert float(grad[2].float().abs().max()) == 0
+    assert gpu_lib.get_status(ws) == 0
+
+
+@pytest.mark.parametrize("vocab", FAR_COLS)
+def test_policy_low_temperature(gpu_lib, vocab):
+    """Logits over a temperature of 2e-38 leave FP32: equal ones are uniform still, and the
+    larger of two is certain."""
+    x = torch.full((2, vocab), 30.0, device="cuda")
+    x[1] = 25.0
+    x[1, vocab // 3] = 30.0
+    t = torch.full((2,), vocab // 3, device="cuda")
+    one = torch.ones(2, device="cuda")
+    out, _ = run_policy(gpu_lib, dict(x=x, t=t, w=one, old=-one, adv=one), None, ref=False,
+                        temperature=2e-38)
+    logv = float(np.log(vocab))
+    assert abs(float(out.logp[0]) + logv) <= 4 * E32 * (logv + 1)
+    assert float(out.logp[1]) == 0
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("vocab", FAR_COLS)
+def test_preference_rows_of_the_lowest_value(gpu_lib, dt, vocab):
+    """Three uniform rows against one (all logits of the type's lowest value)."""
+    x = torch.full((4, vocab), torch.finfo(DT[dt]).min, device="cuda", dtype=DT[dt])
+    t = torch.full((4,), vocab - 1, device="cuda")
+    off = torch.tensor([0, 3, 4], dtype=torch.int32, device="cuda")
+    ref = torch.zeros(2, device="cuda")
+    grad = torch.full_like(x, 3.0)
+    out, ws = run_pref(gpu_lib, x, t, off, ref, grad, beta=0.25, kind=0, smoothing=0.0)
+    logv = float(np.log(vocab))
+    tol = 16 * E32 * (logv + 1)
+    assert abs(float(out.logp[0]) + 3 * logv) <= tol
+    assert abs(float(out.logp[1]) + logv) <= tol
+    assert abs(float(out.margin) + 0.5 * logv) <= tol
+    g = -0.25 / (1 + np.exp(-0.5 * logv))               # d loss / d logp, z = -log(V) / 2
+    shape = torch.full((4, vocab), -1.0 / vocab, device="cuda", dtype=torch.float64)
+    shape[:, vocab - 1] += 1.0
+    want = g * shape
+    want[3] *= -1
+    close(grad, want, (ULP[dt] + tol) * want.abs() + E32 + TINY[dt])
+    assert gpu_lib.get_status(ws) == 0
+
+
+@pytest.mark.parametrize("vocab", [40, 3000])
+@pytest.mark.parametrize("adv", [1.0, -1.0])
+def test_policy_keeps_nan(gpu_lib, vocab, adv):
+    """A row whose ratio is no number (a NaN logit; -inf less -inf) shows in the sums and in
+    its own gradient, and nowhere else."""
+    i = policy_inputs(6, vocab, "f32", masked=0.0)
+    i["adv"][:] = adv
+    i["t"][4] = 1
+    clean = torch.empty_like(i["x"])
+    run_policy(gpu_lib, i, clean, ref=False)
+    for row, set_ in ((2, lambda: i["x"][2].index_fill_(0, torch.tensor([7], device="cuda"),
+                                                        float("nan"))),
+                      (4, lambda: (i["x"][4, 1:2].fill_(float("-inf")),
+                                   i["old"][4:5].fill_(float("-inf"))))):
+        keep = {k: v.clone() for k, v in i.items()}
+        set_()
+        grad = torch.empty_like(clean)
+        out, _ = run_policy(gpu_lib, i, grad, ref=False)
+        assert out.stats[0].isnan() and grad[row].isnan().all()
+        others = [r for r in range(6) if r != row]
+        assert torch.equal(grad[others], clean[others])
+        i = keep
+
+
+def test_group_sums_of_long_depth(gpu_lib):
+    """Tiles whose sums take longer than a wait between stages: one product 2^29 deep, and
+    a weight gradient over 2^28 rows and a ragged end.  Few terms are not zero, so the sums
+    are exact."""
+    k = (1 << 29) + 8
+    x = torch.zeros(1, k, device="cuda", dtype=torch.bfloat16)
+    w = torch.zeros(1, 1, k, device="cuda", dtype=torch.bfloat16)
+    y = torch.empty(1, 1, device="cuda", dtype=torch.bfloat16)
+    for j, at in enumerate([0, 63, 64, 1 << 28, k - 9, k - 1]):
+        x[0, at], w[0, 0, at] = 1.0, 2.0 ** j
+    off = offsets_of([1])
+    ws = gpu_lib.group_workspace(x, w, y)
+    gpu_lib.group_product(x, w, off, y, ws)
+    assert gpu_lib.get_status(ws) == 0
+    assert float(y) == 63.0
+    del x, w
+    rows = (1 << 28) + 5
+    x = torch.zeros(rows, 8, device="cuda", dtype=torch.bfloat16)
+    dy = torch.zeros(rows, 8, device="cuda", dtype=torch.bfloat16)
+    for j, at in enumerate([0, 63, 1 << 27, rows - 6, rows - 1]):
+        x[at, 3], dy[at, 5] = 1.0, 2.0 ** j
+    dw = torch.full((1, 8, 8), 9.0, device="cuda", dtype=torch.bfloat16)
+    ws = gpu_lib.group_workspace(x, dw, dy)
+    gpu_lib.group_product_dw(dy, x, offsets_of([rows]), dw, ws)
+    assert gpu_lib.get_status(ws) == 0
+    want = torch.zeros_like(dw)
+    want[0, 5, 3] = 31.0
+    assert torch.equal(dw, want)

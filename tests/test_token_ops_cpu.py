@@ -202,3 +202,11 @@ def test_binding_refuses_wrong_shapes():
             casgd.policy_loss(*args, pol, qws)
     with pytest.raises(ValueError):
         casgd.policy_loss(f, ids, v, v, v, f, casgd.PolicyOut.alloc(3), qws)
+
+
+@pytest.mark.parametrize("t", [float("inf"), 1e-39])
+def test_policy_refuses_temperatures_without_an_inverse(lib, t):
+    p = nat.PolicyParams(0.0, 0.2, 0.2, t, 1.0)
+    f = [P(FAKE)] * 6
+    assert lib.casgd_policy_loss(C.byref(mat()), C.byref(tok()), *f[:4], C.byref(p), *f[4:], None,
+                                 P(FAKE), 1 << 30, None) == nat.CASGD_ERR_ARG
