@@ -64,6 +64,7 @@ constexpr int kStageBytes = 2 * kHalf;
 constexpr int kMaxGroups = CASGD_MAX_GROUPS;
 constexpr uint64_t kTimeoutNs = 1000000000ull;
 constexpr uint32_t kTmemCols = 2 * BN;
+constexpr int kPanel = 8;
 // Eight epilogue warps, two per quarter of TMEM's lanes: with four, the short tiles of dW
 // (and stores of Y and dX) waited for their epilogue.
 constexpr int kEpiWarps = 8;
@@ -221,8 +222,20 @@ __device__ __forceinline__ Tile tile_at(const GroupTc& a, const Shared* sh, int 
   const int len = kDir == GROUP_DW ? a.k : r.rows;  // N side
   const int nt = (len + BN - 1) / BN;               // equal tiles, multiples of 32
   const int step = ((len + nt - 1) / nt + 31) & ~31;
-  r.m0 = local / nt * BM;
-  r.n0 = local % nt * step;
+  // Panels of kPanel tiles of the N side, all of the M side's tiles in each: the tiles in
+  // work at a time share rows of both sides, so that a group larger than L2 is not read
+  // from memory once per tile of the M side.
+  int w = nt, j0 = 0, at = local;
+  if (nt > kPanel) {
+    const int per = kPanel * (((kDir == GROUP_DX ? a.k : a.n) + BM - 1) / BM);
+    const int panel = local / per;
+    at -= panel * per;
+    j0 = panel * kPanel;
+    w = nt - j0 < kPanel ? nt - j0 : kPanel;
+  }
+  const int mi = at / w;
+  r.m0 = mi * BM;
+  r.n0 = (j0 + at - mi * w) * step;
   r.valid = len - r.n0 < step ? len - r.n0 : step;
   r.n = (r.valid + 31) & ~31;
   r.depth = kDir == GROUP_Y ? a.k : kDir == GROUP_DX ? a.n : r.rows & ~15;
@@ -656,21 +669,52 @@ __global__ void __launch_bounds__(kThreads<kDir>, 1)
 }
 
 // dst (rows x cols8, cols padded to a multiple of 8 with zeros) = src; `parts` matrices.
+// A warp per row.  Granules of 16 bytes of dst whose elements lie in two whole granules of
+// src are shifted together from those; the others, at most 24 elements at the two ends of a
+// row, go one by one.
+__device__ __forceinline__ uint4 shifted(uint4 a, uint4 b, int elems) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  if (elems & 4) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  }
+  if (elems & 2) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  }
+  const int h = 16 * (elems & 1);
+  return make_uint4(__funnelshift_r(w[0], w[1], h), __funnelshift_r(w[1], w[2], h),
+                    __funnelshift_r(w[2], w[3], h), __funnelshift_r(w[3], w[4], h));
+}
 __global__ void __launch_bounds__(256)
     group_pad_kernel(const uint16_t* src, int64_t ld, int64_t stride, int64_t rows, int64_t cols,
                      int64_t parts, uint16_t* dst) {
   wait_prior_grid();
   allow_next_grid();
-  const int64_t groups = (cols + 7) / 8;
-  const int64_t total = parts * rows * groups;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
-       i += (int64_t)gridDim.x * 256) {
-    const int64_t g = i % groups, r = i / groups;
-    const uint16_t* s = src + r / rows * stride + r % rows * ld + g * 8;
-    Pack<uint16_t, 8> v;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v.v[j] = g * 8 + j < cols ? s[j] : (uint16_t)0;
-    *reinterpret_cast<Pack<uint16_t, 8>*>(dst + i * 8) = v;
+  const int lane = threadIdx.x & 31;
+  const int64_t wide = (cols + 7) / 8 * 8;
+  for (int64_t r = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 5; r < parts * rows;
+       r += (int64_t)gridDim.x * 8) {
+    const int64_t part = parts > 1 ? r / rows : 0;
+    const uint16_t* s = src + part * stride + (r - part * rows) * ld;
+    uint16_t* d = dst + r * wide;
+    const int off = (int)((reinterpret_cast<uintptr_t>(s) & 15) / 2);
+    // granules [g0, g1) of dst: src elements 8 g - off .. 8 g - off + 15 (7 if off is 0) are
+    // the row's
+    const int64_t g0 = off ? 1 : 0, need = off ? 16 : 8;
+    int64_t g1 = cols + off < need ? 0 : (cols + off - need) / 8 + 1;
+    if (g1 < g0) g1 = g0;
+#pragma unroll 4
+    for (int64_t g = g0 + lane; g < g1; g += 32) {
+      const uint4* q = reinterpret_cast<const uint4*>(s + 8 * g - off);
+      const uint4 lo = q[0], hi = off ? q[1] : lo;
+      *reinterpret_cast<uint4*>(d + 8 * g) = shifted(lo, hi, off);
+    }
+    const int64_t ends = 8 * g0 + wide - 8 * g1;
+    for (int64_t i = lane; i < ends; i += 32) {
+      const int64_t e = i < 8 * g0 ? i : i + 8 * (g1 - g0);
+      if (e < wide) d[e] = e < cols ? s[e] : (uint16_t)0;
+    }
   }
 }
 
