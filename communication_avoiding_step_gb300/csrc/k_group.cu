@@ -257,18 +257,10 @@ __device__ __forceinline__ uint32_t pack2<__half>(uint32_t lo, uint32_t hi) {
   return reinterpret_cast<const uint32_t&>(v);
 }
 
-// The first `count` of eight 16-bit values to dst, one by one.
-__device__ __forceinline__ void store_some(uint16_t* dst, uint4 v, int count) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (j < count) dst[j] = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
-}
-
 // dW: one warp's 32 rows (n) of a tile, `rows` x `cols` of them real, every other 64
 // columns from c0 on.  One row per lane into a staging buffer (16-byte chunk c of row r at
 // slot c ^ (r % 8), so neither side has bank conflicts), then four rows of 128 bytes per
-// store.
+// store, or (rows that do not start on 16 bytes, a row's last columns) 32 elements of one.
 template <class T>
 __device__ __forceinline__ void store_rows(const GroupTc& a, uint16_t* out, int rows, int cols,
                                            int c0, uint32_t taddr, bool zero, uint8_t* stage,
@@ -297,33 +289,43 @@ __device__ __forceinline__ void store_rows(const GroupTc& a, uint16_t* out, int 
       *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) * 16)) = v;
     }
     __syncwarp();
-    const int c = lane & 7, r0 = lane >> 3;
-    uint16_t* dst = out + (int64_t)r0 * a.ldo + c0 + 8 * c;
-    const int left = cols - c0 - 8 * c;
-    const bool vec = a.vec_out && cols - c0 >= 64;  // (of the whole warp)
+    if (a.vec_out && cols - c0 >= 64) {
+      const int c = lane & 7, r0 = lane >> 3;
+      uint16_t* dst = out + (int64_t)r0 * a.ldo + c0 + 8 * c;
 #pragma unroll
-    for (int i = 0; i < 8; ++i, dst += 4 * a.ldo) {
-      const int r = 4 * i + r0;
-      const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((c ^ (r & 7)) * 16));
-      if (r >= rows) continue;
-      if (vec)
-        *reinterpret_cast<uint4*>(dst) = v;
-      else
-        store_some(dst, v, left);
+      for (int i = 0; i < 8; ++i, dst += 4 * a.ldo) {
+        const int r = 4 * i + r0;
+        const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((c ^ (r & 7)) * 16));
+        if (r < rows) *reinterpret_cast<uint4*>(dst) = v;
+      }
+    } else {
+      uint16_t* dst = out + c0 + lane;
+      const int most = rows < 32 ? rows : 32;
+#pragma unroll 4
+      for (int r = 0; r < most; ++r, dst += a.ldo) {
+#pragma unroll
+        for (int h = 0; h < 64; h += 32) {
+          const int c = (lane + h) >> 3;
+          const uint16_t v = *reinterpret_cast<const uint16_t*>(
+              stage + r * 128 + ((c ^ (r & 7)) * 16) + (lane & 7) * 2);
+          if (c0 + h + lane < cols) dst[h] = v;
+        }
+      }
     }
   }
 }
 
 // Y, dX: one warp's 32 columns of the output (TMEM lanes), `cols` of them real, for every
 // other 32 tokens (TMEM columns) from t0 on.  A lane's column of each token into the
-// staging buffer, then eight tokens' 64-byte segments per store.
+// staging buffer, then eight tokens' 64-byte segments per store, or (rows that do not start
+// on 16 bytes, a row's last columns) one token's 32 elements.
 template <class T>
 __device__ __forceinline__ void store_tokens(const GroupTc& a, uint16_t* out, int tokens, int cols,
                                              int t0, uint32_t taddr, bool zero, uint8_t* stage,
                                              int lane) {
   uint16_t* st = reinterpret_cast<uint16_t*>(stage);
   const int col = (lane & 3) * 8;
-  const bool vec = a.vec_out && cols >= 32;  // (of the whole warp)
+  const bool vec = a.vec_out && cols >= 32;
   for (; t0 < tokens; t0 += 64) {
     uint32_t v[32];
     if (!zero) {
@@ -342,16 +344,20 @@ __device__ __forceinline__ void store_tokens(const GroupTc& a, uint16_t* out, in
       st[(e + 1) * 32 + lane] = (uint16_t)(p >> 16);
     }
     __syncwarp();
-    uint16_t* dst = out + (int64_t)(t0 + (lane >> 2)) * a.ldo + col;
+    if (vec) {
+      uint16_t* dst = out + (int64_t)(t0 + (lane >> 2)) * a.ldo + col;
 #pragma unroll
-    for (int i = 0; i < 4; ++i, dst += 8 * a.ldo) {
-      const int t = 8 * i + (lane >> 2);
-      const uint4 w = *reinterpret_cast<const uint4*>(st + t * 32 + col);
-      if (t0 + t >= tokens) continue;
-      if (vec)
-        *reinterpret_cast<uint4*>(dst) = w;
-      else
-        store_some(dst, w, cols - col);
+      for (int i = 0; i < 4; ++i, dst += 8 * a.ldo) {
+        const int t = 8 * i + (lane >> 2);
+        const uint4 w = *reinterpret_cast<const uint4*>(st + t * 32 + col);
+        if (t0 + t < tokens) *reinterpret_cast<uint4*>(dst) = w;
+      }
+    } else {
+      uint16_t* dst = out + (int64_t)t0 * a.ldo + lane;
+      const int most = tokens - t0 < 32 ? tokens - t0 : 32;
+#pragma unroll 4
+      for (int t = 0; t < most; ++t, dst += a.ldo)
+        if (lane < cols) *dst = st[t * 32 + lane];
     }
   }
 }
@@ -704,11 +710,19 @@ __global__ void __launch_bounds__(256)
     const int64_t g0 = off ? 1 : 0, need = off ? 16 : 8;
     int64_t g1 = cols + off < need ? 0 : (cols + off - need) / 8 + 1;
     if (g1 < g0) g1 = g0;
-#pragma unroll 4
-    for (int64_t g = g0 + lane; g < g1; g += 32) {
-      const uint4* q = reinterpret_cast<const uint4*>(s + 8 * g - off);
-      const uint4 lo = q[0], hi = off ? q[1] : lo;
-      *reinterpret_cast<uint4*>(d + 8 * g) = shifted(lo, hi, off);
+    constexpr int kU = 4;  // loads in flight
+    for (int64_t g = g0 + lane; g < g1; g += 32 * kU) {
+      uint4 lo[kU], hi[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const uint4* q = reinterpret_cast<const uint4*>(s + 8 * (g + 32 * u) - off);
+        if (g + 32 * u < g1) lo[u] = q[0];
+        if (g + 32 * u < g1 && off) hi[u] = q[1];
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+        if (g + 32 * u < g1)
+          *reinterpret_cast<uint4*>(d + 8 * (g + 32 * u)) = shifted(lo[u], hi[u], off);
     }
     const int64_t ends = 8 * g0 + wide - 8 * g1;
     for (int64_t i = lane; i < ends; i += 32) {
