@@ -107,16 +107,19 @@ cudaError_t embed_from(const Mat& t, Ids ids, float s, int64_t pad, const Mat& o
 // Stable radix sort of (token, position) pairs, least significant digit first.  A token
 // that is dropped (padding, or out of range) sorts last, with the key `vocab`.
 //
-// Up to kMaxCluster * kTile tokens: one launch.  A cluster sorts, a tile of kTile pairs
-// per CTA; per pass the CTAs read one another's digit counts through distributed shared
+// Up to kClusterRows tokens: one launch.  A cluster sorts, a tile of up to 8192 pairs per
+// CTA; per pass the CTAs read one another's digit counts through distributed shared
 // memory, scatter through global memory (L2) and meet at a cluster barrier.  The other
 // CTAs of the launch clear the gradient meanwhile, which hides the sort wherever the
 // table takes longer to clear.  More tokens: one launch that counts the first digit (and
-// clears), then one per pass.  There a tile's scatter base comes from the per-tile counts
-// in global memory, which the scatter of a pass keeps for the next pass's tiles.
+// clears), then one per pass, in up to kManyTiles tiles where they are enough.  There a
+// tile's scatter base comes from the per-tile counts in global memory, which the scatter
+// of a pass keeps for the next pass's tiles.  (Launches from 32,768 tokens on: 60,000 x
+// 2048 into 30,000 rows 134 -> 158 us; 41,654 x 429 into 2558 rows 60 -> 55.)
 constexpr int kSortThreads = 1024;
 constexpr int kSortItems = 8;  // per thread
-constexpr int kTile = kSortThreads * kSortItems;
+constexpr int64_t kClusterRows = 8 * kSortThreads * kSortItems;
+constexpr int64_t kManyTiles = 64;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxRadix = 512;
 constexpr int kMaxCluster = 8;
@@ -151,9 +154,10 @@ GradLayout grad_layout(int64_t rows, int64_t vocab, int64_t dim) {
   const int64_t per = (rows + L.tiles - 1) / L.tiles;
   L.items = (int)((per + kSortThreads - 1) / kSortThreads);
   if (L.items < 1) L.items = 1;
-  if (L.items > kSortItems) {
-    L.items = kSortItems;
-    L.tiles = (rows + kTile - 1) / kTile;
+  if (rows > kClusterRows) {
+    for (L.items = 1; L.items < kSortItems && rows > kManyTiles * L.items * kSortThreads;)
+      L.items *= 2;
+    L.tiles = (rows + L.items * kSortThreads - 1) / (L.items * kSortThreads);
   }
   // Chunk length: enough chunks to fill the GPU, few enough partial sums for long lists
   // (60,000 tokens of 2048 columns: 136 us with up to 2048 chunks, 166 us with up to 4096).
@@ -163,7 +167,7 @@ GradLayout grad_layout(int64_t rows, int64_t vocab, int64_t dim) {
   const SortPlan p = sort_plan(vocab);
   size_t o = align_up(sizeof(Ctrl));
   L.off_count = o;  // per-tile counts, for lists that one cluster does not sort
-  if (L.tiles > kMaxCluster) o += align_up((size_t)p.passes * L.tiles * p.radix() * 4);
+  if (rows > kClusterRows) o += align_up((size_t)p.passes * L.tiles * p.radix() * 4);
   L.off_owner = o;  // word 0: how many; then (first chunk, end chunk) of every run that
   o += align_up((size_t)(2 * L.chunks + 2) * 4);  // crosses a chunk border
   for (int i = 0; i < 2; ++i) {
@@ -390,8 +394,8 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortArgs a, Cl
   bool bad = false;
 #pragma unroll
   for (int j = 0; j < kSortItems; ++j) {
-    const int64_t i = (int64_t)blockIdx.x * kTile + j * kSortThreads + threadIdx.x;
-    if (i < a.rows) atomicAdd(&cnt[sort_key(a, i, bad) & (radix - 1)], 1u);
+    const int64_t i = ((int64_t)blockIdx.x * a.items + j) * kSortThreads + threadIdx.x;
+    if (j < a.items && i < a.rows) atomicAdd(&cnt[sort_key(a, i, bad) & (radix - 1)], 1u);
   }
   if (bad) set_status(a.ctrl, ST_BAD_INDEX);
   __syncthreads();
@@ -405,7 +409,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(SortArgs a, 
   wait_prior_grid();
   allow_next_grid();
   const int radix = 1 << a.bits, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t tile = blockIdx.x, w0 = tile * kTile + (int64_t)warp * kSortItems * 32;
+  const int64_t tile = blockIdx.x, w0 = (tile * kSortWarps + warp) * a.items * 32;
   const bool odd = pass & 1;
   const uint32_t *ki = odd ? a.key[0] : a.key[1], *pi = odd ? a.pos[0] : a.pos[1];
   uint32_t *ko = odd ? a.key[1] : a.key[0], *po = odd ? a.pos[1] : a.pos[0];
@@ -414,8 +418,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(SortArgs a, 
   for (int j = 0; j < kSortItems; ++j) {
     const int64_t i = w0 + j * 32 + lane;
     bool bad = false;
-    t.key[j] = i >= a.rows ? 0u : pass ? ki[i] : sort_key(a, i, bad);
-    t.pos[j] = i >= a.rows || !pass ? (uint32_t)i : pi[i];
+    const bool in = j < a.items && i < a.rows;
+    t.key[j] = !in ? 0u : pass ? ki[i] : sort_key(a, i, bad);
+    t.pos[j] = !in || !pass ? (uint32_t)i : pi[i];
   }
   for (int i = threadIdx.x; i < kSortWarps * kMaxRadix / 8; i += kSortThreads)
     reinterpret_cast<uint4*>(&s.cnt[0][0])[i] = make_uint4(0, 0, 0, 0);
@@ -431,20 +436,20 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(SortArgs a, 
     }
   }
   __syncthreads();
-  rank_tile(t, kSortItems, w0, a.rows, pass * a.bits, radix, s.cnt[warp]);
+  rank_tile(t, a.items, w0, a.rows, pass * a.bits, radix, s.cnt[warp]);
   __syncthreads();
   sum_warps(s, radix, s.total[0]);
   scan_digits(s, radix, all, before);
   uint32_t* next = pass + 1 < a.passes ? a.count + (int64_t)(pass + 1) * a.tiles * radix : nullptr;
 #pragma unroll
   for (int j = 0; j < kSortItems; ++j) {
-    if (w0 + j * 32 + lane >= a.rows) continue;
+    if (j >= a.items || w0 + j * 32 + lane >= a.rows) continue;
     const uint32_t d = (t.key[j] >> (pass * a.bits)) & (radix - 1);
     const uint32_t to = s.base[d] + s.cnt[warp][d] + t.rank[j];
     ko[to] = t.key[j];
     po[to] = t.pos[j];
     if (next)
-      atomicAdd(&next[(int64_t)(to / kTile) * radix +
+      atomicAdd(&next[(int64_t)(to / (uint32_t)(a.items * kSortThreads)) * radix +
                       ((t.key[j] >> ((pass + 1) * a.bits)) & (radix - 1))],
                 1u);
   }
@@ -776,12 +781,12 @@ cudaError_t sum_from(const Mat& d, const Mat& g, const GradArgs& a, Ctrl* ctrl, 
 cudaError_t launch_sort(const SortArgs& a, const ClearArgs& clear, Ctx& c) {
   const size_t smem = sizeof(SortShared);
   cudaError_t e = cudaFuncSetAttribute(
-      a.tiles <= kMaxCluster ? (const void*)sort_kernel : (const void*)sort_scatter_kernel,
+      a.rows <= kClusterRows ? (const void*)sort_kernel : (const void*)sort_scatter_kernel,
       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   int64_t blocks = (clear.rows + kSortWarps - 1) / kSortWarps;  // a warp per row at most
   if (blocks > 2 * c.num_sms) blocks = 2 * c.num_sms;
-  if (a.tiles > kMaxCluster) {
+  if (a.rows > kClusterRows) {
     e = launch(c, a.tiles + blocks, dim3(kSortThreads), sort_count_kernel, a, clear);
     for (int p = 0; p < a.passes && e == cudaSuccess; ++p) {
       cudaLaunchConfig_t cfg = {};
