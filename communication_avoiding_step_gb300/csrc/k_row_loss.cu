@@ -392,11 +392,11 @@ __global__ void __launch_bounds__(kBlock) pref_pair_kernel(PrefArgs a, PrefWs w)
   for (int q = 0; q < 2; ++q) {
     double s = 0.0;
     int n = 0;
+#pragma unroll 4
     for (int64_t t = o[q] + threadIdx.x; t < o[q + 1]; t += kBlock) {
       const int64_t target = a.targets.at(t);
-      if (target < 0 || target >= a.logits.cols) continue;
-      s += w.lp[t];
-      ++n;
+      s += w.lp[t];  // (0 in a masked row)
+      n += target >= 0 && target < a.logits.cols;
     }
 #pragma unroll
     for (int h = 16; h > 0; h /= 2) {
@@ -439,17 +439,23 @@ __global__ void __launch_bounds__(kBlock) pref_pair_kernel(PrefArgs a, PrefWs w)
   }
   __syncthreads();
   for (int q = 0; q < 2; ++q)
+#pragma unroll 4
     for (int64_t t = o[q] + threadIdx.x; t < o[q + 1]; t += kBlock) {
       const int64_t target = a.targets.at(t);
       if (target >= 0 && target < a.logits.cols) w.coef[t] = coef[q];
     }
-  if (last && warp == 0) {  // every pair's loss is in: their mean, in a fixed order
+  if (last) {  // every pair's loss is in: their mean, in a fixed order
     __threadfence();
     double s = 0.0;
-    for (int64_t i = lane; i < a.pairs; i += 32) s += __ldcg(&w.loss[i]);
+#pragma unroll 4
+    for (int64_t i = threadIdx.x; i < a.pairs; i += kBlock) s += __ldcg(&w.loss[i]);
 #pragma unroll
     for (int h = 16; h > 0; h /= 2) s += __shfl_xor_sync(0xffffffffu, s, h);
-    if (lane == 0) {
+    if (lane == 0) ssum[0][warp] = s;  // (read by thread 0 before the last barrier)
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      s = 0.0;
+      for (int i = 0; i < kWarps; ++i) s += ssum[0][i];
       a.loss[0] = (float)(s / (double)a.pairs);
       w.ctrl->loss_done = 0;
     }
@@ -471,9 +477,10 @@ __global__ void __launch_bounds__(kBlock, 3) pref_grad_warp_kernel(PrefArgs a, P
 }
 
 // ------------------------------------------------------------------ policy loss
+constexpr int kMaxBlocks = 1024;
 struct PolicyWs {
   Ctrl* ctrl;
-  float *loss, *kl, *clipped;  // per row
+  double* part;  // per block: loss, KL term, weight of the clipped rows
 };
 
 // What the policy loss reads of a row beside its logits.
@@ -525,31 +532,47 @@ __device__ __forceinline__ RowLoss policy_row(const PolicyArgs& a, const RowInfo
   return o;
 }
 
-__device__ __forceinline__ void put_row_loss(const PolicyArgs& a, const PolicyWs& w, int64_t t,
-                                             const RowLoss& o) {
-  a.logp[t] = o.lp;
-  w.loss[t] = o.loss;
-  w.kl[t] = o.kl;
-  w.clipped[t] = o.clipped;
-}
+// The sums of the rows that a thread has finished, in the order that it takes them in.
+struct PolicySums {
+  double v[3] = {0.0, 0.0, 0.0};
+  __device__ __forceinline__ void add(const RowLoss& o) {
+    v[0] += o.loss;
+    v[1] += o.kl;
+    v[2] += o.clipped;
+  }
+};
 
-// The last block to come here adds the rows' terms in a fixed order.  Called by the first
-// kBlock threads of every block (named barrier 1).
-__device__ void policy_sums(const PolicyArgs& a, const PolicyWs& w) {
+// Adds the blocks' sums up: those of a block's warps (lane 0 of each; zeros where it has
+// finished no row) in order, then, by the last block to come here, the blocks'.  A block's
+// rows depend on the grid alone, so the order is fixed.  Called by the first kBlock threads
+// of every block (named barrier 1).
+__device__ void policy_sums(const PolicyArgs& a, const PolicyWs& w, const PolicySums& mine) {
   __shared__ int last;
   __shared__ double red[3][kBlock / 32];
   auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(kBlock) : "memory"); };
-  __threadfence();
+#pragma unroll
+  for (int e = 0; e < 3; ++e)
+    if ((threadIdx.x & 31) == 0) red[e][threadIdx.x >> 5] = mine.v[e];
   meet();
-  if (threadIdx.x == 0) last = atomicAdd(&w.ctrl->loss_done, 1u) == gridDim.x - 1;
+  if (threadIdx.x == 0) {
+    for (int e = 0; e < 3; ++e) {
+      double v = 0.0;
+      for (int i = 0; i < kBlock / 32; ++i) v += red[e][i];
+      w.part[3 * blockIdx.x + e] = v;
+    }
+    __threadfence();
+    last = atomicAdd(&w.ctrl->loss_done, 1u) == gridDim.x - 1;
+  }
   meet();
   if (!last) return;
   __threadfence();
   double s[3] = {0, 0, 0};
-  for (int64_t t = threadIdx.x; t < a.logits.rows; t += kBlock) {
-    s[0] += __ldcg(&w.loss[t]);
-    s[1] += __ldcg(&w.kl[t]);
-    s[2] += __ldcg(&w.clipped[t]);
+#pragma unroll
+  for (int i = 0; i < kMaxBlocks / kBlock; ++i) {
+    const int b = i * kBlock + (int)threadIdx.x;
+#pragma unroll
+    for (int e = 0; e < 3; ++e)
+      if (b < (int)gridDim.x) s[e] += __ldcg(&w.part[3 * b + e]);
   }
 #pragma unroll
   for (int e = 0; e < 3; ++e) {
@@ -572,6 +595,7 @@ __global__ void __launch_bounds__(kBlock, 3) policy_warp_kernel(PolicyArgs a, Po
   allow_next_grid();
   const int lane = threadIdx.x & 31;
   const float inv_t = 1.0f / a.temperature, scale = kLog2e * inv_t;
+  PolicySums sums;
   for (int64_t t = ((int64_t)blockIdx.x * kBlock + threadIdx.x) >> 5; t < a.logits.rows;
        t += (int64_t)gridDim.x * (kBlock / 32)) {
     RowInfo f;
@@ -586,13 +610,14 @@ __global__ void __launch_bounds__(kBlock, 3) policy_warp_kernel(PolicyArgs a, Po
     const RowLoss o = policy_row(a, f, r, inv_t, scale);
     if (lane == 0) {
       if (bad) set_status(w.ctrl, ST_BAD_INDEX);
-      put_row_loss(a, w, t, o);
+      a.logp[t] = o.lp;
+      sums.add(o);
     }
     if (a.grad.p)
       warp_grad(row, static_cast<T*>(a.grad.p) + t * a.grad.ld, lane, scale, r, f.target, o.g,
                 f.weight == 0.0f || o.none());
   }
-  policy_sums(a, w);
+  policy_sums(a, w, sums);
 }
 
 // ------------------------------------------------------------------ rows through a ring
@@ -775,6 +800,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) stream_kernel(A a, W w) {
     }
   };
   bool ok = true;
+  PolicySums sums;  // (STREAM_POLICY, thread 0)
   for (int64_t i = 0; i < mine; ++i) {
     const int64_t t = row_at(i);
     const Row<T> row(logits + t * a.logits.ld, a.logits.cols);
@@ -827,7 +853,8 @@ __global__ void __launch_bounds__(kStreamThreads, 2) stream_kernel(A a, W w) {
         if constexpr (kMode == STREAM_POLICY) {
           o = policy_row(a, f, r, inv_t, scale);
           if (lane == 0) {
-            put_row_loss(a, w, t, o);
+            a.logp[t] = o.lp;
+            sums.add(o);
             sh->sum = r;
             sh->loss = o;
           }
@@ -894,7 +921,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) stream_kernel(A a, W w) {
     if (!zero && (whole ? (tg - row.whole0) % kBlock == tid : tg == edge))
       out[f.target] = Elem<T>::put(target_grad(g, f.xt, r, scale));
   }
-  if constexpr (kMode == STREAM_POLICY) policy_sums(a, w);
+  if constexpr (kMode == STREAM_POLICY) policy_sums(a, w, sums);
 }
 
 template <class... P, class... A>
@@ -910,6 +937,7 @@ cudaError_t launch(Ctx& c, unsigned grid, unsigned block, void (*fn)(P...), A...
 }
 
 unsigned blocks_for(int64_t items, int64_t most) {
+  if (most > kMaxBlocks) most = kMaxBlocks;
   return (unsigned)(items < 1 ? 1 : items < most ? items : most);
 }
 
@@ -959,7 +987,8 @@ size_t preference_workspace_bytes(int64_t rows, int64_t pairs) {
   return pref_layout(rows, pairs).total;
 }
 size_t policy_workspace_bytes(int64_t rows) {
-  return align_up(sizeof(Ctrl)) + 3 * align_up((size_t)rows * 4);
+  (void)rows;
+  return align_up(sizeof(Ctrl)) + align_up(3 * kMaxBlocks * sizeof(double));
 }
 
 cudaError_t launch_preference(const PrefArgs& p, void* ws, Ctx& c) {
@@ -975,9 +1004,7 @@ cudaError_t launch_preference(const PrefArgs& p, void* ws, Ctx& c) {
 
 cudaError_t launch_policy(const PolicyArgs& p, void* ws, Ctx& c) {
   char* b = static_cast<char*>(ws) + align_up(sizeof(Ctrl));
-  const size_t step = align_up((size_t)p.logits.rows * 4);
-  const PolicyWs w{static_cast<Ctrl*>(ws), reinterpret_cast<float*>(b),
-                   reinterpret_cast<float*>(b + step), reinterpret_cast<float*>(b + 2 * step)};
+  const PolicyWs w{static_cast<Ctrl*>(ws), reinterpret_cast<double*>(b)};
   if (p.logits.dtype == CASGD_F32) return policy_typed<float>(p, w, c);
   if (p.logits.dtype == CASGD_BF16) return policy_typed<__nv_bfloat16>(p, w, c);
   return policy_typed<__half>(p, w, c);
