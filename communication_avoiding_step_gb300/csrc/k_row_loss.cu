@@ -16,8 +16,8 @@
 //   holds comes first.
 // Measured, BF16, 128,000 columns: policy 8192 rows 765 us (5.2 TB/s of one read and one
 // write); preference 12,288 rows 1385 us (6.4 TB/s of two reads and one write).
-// Rows wider than kWarpCols go through stream_kernel, a ring of bulk copies per block;
-// shorter ones take a warp each (warp kernels), without shared memory.
+// Long rows go through stream_kernel, a ring of bulk copies per block; short ones take a
+// warp each (warp kernels), without shared memory.
 //
 // Rows are handled in 16-byte granules of memory, counted from the granule that holds the
 // row's first element, so that rows at any alignment take the same path; the granules that
@@ -260,21 +260,45 @@ __device__ __forceinline__ Granule softmax_part(const Granule& x, float scale, f
   return o;
 }
 
-// Maximum and sum of a row by a warp; every lane gets them.
+// A row by a warp: lanes take its whole granules in turn, kWarpU of them at once, lanes 0
+// and 31 the granules at its ends that hold elements of other rows too.
+constexpr int kWarpU = 4;
+struct Held {  // the granules of the batch read last
+  Granule p[kWarpU];
+};
 template <class T>
-__device__ __forceinline__ MaxSum warp_max_sum(const Row<T>& r, int lane, float scale) {
-  constexpr int kU = 4;
-  MaxSum acc{-INFINITY, 0.0f};
-  int g = lane;
-  for (; g + 32 * (kU - 1) < r.granules; g += 32 * kU) {
-    Granule p[kU];
+__device__ __forceinline__ int warp_edge(const Row<T>& r, int lane) {
+  if (lane == 0 && r.whole0 > 0) return 0;
+  if (lane == 31 && r.whole1 < r.granules && (r.granules > 1 || r.whole0 == 0))
+    return r.granules - 1;
+  return -1;
+}
+template <class T>
+__device__ __forceinline__ void warp_batch(const Row<T>& r, int g, Held& h) {
 #pragma unroll
-    for (int u = 0; u < kU; ++u) p[u] = r.load(g + 32 * u);
-    acc = join(acc, granules_max_sum<T, kU>(p, scale), scale);
+  for (int u = 0; u < kWarpU; ++u) {
+    h.p[u] = no_granule<T>();
+    if (g + 32 * u < r.whole1)
+      h.p[u] = *reinterpret_cast<const Granule*>(r.x + r.first(g + 32 * u));
   }
-#pragma unroll 1
-  for (; g < r.granules; g += 32) {
-    const Granule p[1] = {r.load(g)};
+}
+// Its maximum and sum; every lane gets them.
+template <class T>
+__device__ __forceinline__ MaxSum warp_max_sum(const Row<T>& r, int lane, float scale, Held& h) {
+  MaxSum acc{-INFINITY, 0.0f};
+  int g = r.whole0 + lane;
+  for (; g + 32 < r.whole1; g += 32 * kWarpU) {
+    warp_batch(r, g, h);
+    acc = join(acc, granules_max_sum<T, kWarpU>(h.p, scale), scale);
+  }
+  if (g < r.whole1) {  // one more (62,748 rows of 184 FP16 columns: 61 us, as a batch 67)
+    h.p[0] = *reinterpret_cast<const Granule*>(r.x + r.first(g));
+    const Granule p[1] = {h.p[0]};
+    acc = join(acc, granules_max_sum<T, 1>(p, scale), scale);
+  }
+  const int edge = warp_edge(r, lane);
+  if (edge >= 0) {
+    const Granule p[1] = {r.load(edge)};
     acc = join(acc, granules_max_sum<T, 1>(p, scale), scale);
   }
   return join_lanes<32>(acc, scale);
@@ -294,20 +318,31 @@ __device__ __forceinline__ float target_grad(float g, float xt, MaxSum r, float 
   return g * (1.0f - fast_exp2(exponent(xt, r.m, scale)) / r.s);
 }
 
-// Writes g * (onehot - softmax), or zeros, to a row by a warp.
+// Writes g * (onehot - softmax), or zeros, to a row by a warp.  held: the row's whole
+// granules are in h.
 template <class T>
 __device__ __forceinline__ void warp_grad(const Row<T>& r, T* out, int lane, float scale,
-                                          MaxSum ms, int64_t target, float g, bool zero) {
+                                          MaxSum ms, int64_t target, float g, bool zero, Held& h,
+                                          bool held) {
   const bool al = same_phase(r.x, out);
   const float k = -g / ms.s;
+  const int edge = warp_edge(r, lane);
+  // the lane that stores the target's granule sets the target
   const int tg = zero ? -1 : (int)((target + r.shift) / Row<T>::kV);
-  const bool mine = tg >= 0 && tg % 32 == lane;
+  const bool mine =
+      tg >= 0 && (r.whole(tg) ? (tg - r.whole0) % 32 == lane : tg == edge);
   const float xt = mine ? Elem<T>::get(r.x[target]) : 0.0f;  // (before the row is written)
-#pragma unroll 2
-  for (int i = lane; i < r.granules; i += 32)
-    put_granule(r, out, al, i, zero ? Granule{{0u, 0u, 0u, 0u}}
-                                    : softmax_part<T>(r.load(i), scale, ms.m, k));
-  // the lane that stored the target's granule sets the target
+  for (int i = r.whole0 + lane; i < r.whole1; i += 32 * kWarpU) {
+    if (!held && !zero) warp_batch(r, i, h);
+#pragma unroll
+    for (int u = 0; u < kWarpU; ++u)
+      if (i + 32 * u < r.whole1)
+        put_granule(r, out, al, i + 32 * u, zero ? Granule{{0u, 0u, 0u, 0u}}
+                                                 : softmax_part<T>(h.p[u], scale, ms.m, k));
+  }
+  if (edge >= 0)
+    put_granule(r, out, al, edge, zero ? Granule{{0u, 0u, 0u, 0u}}
+                                       : softmax_part<T>(r.load(edge), scale, ms.m, k));
   if (mine) out[target] = Elem<T>::put(target_grad(g, xt, ms, scale));
 }
 
@@ -334,9 +369,10 @@ struct PrefWs {
 };
 
 constexpr int kBlock = 256;
-// Up to this many columns a warp takes a row, else a block: a block's barriers and copies
-// cost more than a warp's longer loop there.
-constexpr int64_t kWarpCols = 2048;
+// Rows up to this length are a warp's where there are enough of them to fill the GPU's
+// warps, or kFewWarpBytes where there are not; longer ones are a block's.  A block's
+// barriers cost more than a warp's longer loop there.
+constexpr int64_t kWarpBytes = 16384, kFewWarpBytes = 4096, kRowsPerSm = 8;
 
 __device__ __forceinline__ void put_stats(const PrefWs& w, int64_t t, MaxSum r, float lp) {
   w.m[t] = r.m;
@@ -358,7 +394,8 @@ __global__ void __launch_bounds__(kBlock, 3) pref_stats_warp_kernel(PrefArgs a, 
   float lp = 0.0f;
   if (target >= 0 && !bad) {
     const Row<T> row(static_cast<const T*>(a.logits.p) + t * a.logits.ld, a.logits.cols);
-    r = warp_max_sum<T>(row, lane, kLog2e);
+    Held h;
+    r = warp_max_sum<T>(row, lane, kLog2e, h);
     lp = log_prob(Elem<T>::get(row.x[target]), r, kLog2e);
   }
   if (lane == 0) {
@@ -471,9 +508,10 @@ __global__ void __launch_bounds__(kBlock, 3) pref_grad_warp_kernel(PrefArgs a, P
   const int64_t t = a.logits.rows - 1 - i, target = a.targets.at(t);
   const float g = w.coef[t];
   const Row<T> row(static_cast<const T*>(a.logits.p) + t * a.logits.ld, a.logits.cols);
+  Held h;
   warp_grad(row, static_cast<T*>(a.grad.p) + t * a.grad.ld, threadIdx.x & 31, kLog2e,
             {w.m[t], w.s[t]}, target, g,
-            target < 0 || target >= a.logits.cols || g == 0.0f);
+            target < 0 || target >= a.logits.cols || g == 0.0f, h, false);
 }
 
 // ------------------------------------------------------------------ policy loss
@@ -602,10 +640,11 @@ __global__ void __launch_bounds__(kBlock, 3) policy_warp_kernel(PolicyArgs a, Po
     const bool bad = load_info(a, t, f);
     const Row<T> row(static_cast<const T*>(a.logits.p) + t * a.logits.ld, a.logits.cols);
     MaxSum r{0.0f, 1.0f};
+    Held h;
     f.xt = 0.0f;
     if (f.target >= 0) {
       f.xt = Elem<T>::get(row.x[f.target]);
-      r = warp_max_sum<T>(row, lane, scale);
+      r = warp_max_sum<T>(row, lane, scale, h);
     }
     const RowLoss o = policy_row(a, f, r, inv_t, scale);
     if (lane == 0) {
@@ -615,7 +654,7 @@ __global__ void __launch_bounds__(kBlock, 3) policy_warp_kernel(PolicyArgs a, Po
     }
     if (a.grad.p)
       warp_grad(row, static_cast<T*>(a.grad.p) + t * a.grad.ld, lane, scale, r, f.target, o.g,
-                f.weight == 0.0f || o.none());
+                f.weight == 0.0f || o.none(), h, row.whole1 - row.whole0 <= 32 * kWarpU);
   }
   policy_sums(a, w, sums);
 }
@@ -628,13 +667,13 @@ __global__ void __launch_bounds__(kBlock, 3) policy_warp_kernel(PolicyArgs a, Po
 // other eight warps sum a stage or turn it into gradients.  Granules shared with other rows
 // (at most the first and the last) are read and written element by element by two threads.
 enum StreamMode { STREAM_STATS, STREAM_GRAD, STREAM_POLICY };
-constexpr int kStages = 6;
 constexpr int kU = 4;                       // granules per thread and stage
 constexpr int kStageGranules = kBlock * kU;
 constexpr int kWarps = kBlock / 32;
 constexpr int kStreamThreads = kBlock + 32;
 constexpr uint64_t kTimeoutNs = 1000000000ull;
 
+template <int kStages>
 struct StreamShared {
   uint64_t full[kStages], empty[kStages];
   RowInfo info[kStages];
@@ -643,11 +682,14 @@ struct StreamShared {
   RowLoss loss;
   volatile uint32_t abort;
 };
-constexpr size_t kStreamSmem = (size_t)kStages * kStageGranules * 16 + sizeof(StreamShared);
+template <int kStages>
+constexpr size_t kStreamSmem =
+    (size_t)kStages * kStageGranules * 16 + sizeof(StreamShared<kStages>);
 
 // Bounded wait by a whole warp; false if the phase does not complete in time or the block
 // gave up.
-__device__ __forceinline__ bool stage_wait(uint64_t* bar, uint32_t parity, StreamShared* sh,
+template <class Shared>
+__device__ __forceinline__ bool stage_wait(uint64_t* bar, uint32_t parity, Shared* sh,
                                            Ctrl* ctrl) {
   bool ok = false;
   uint64_t t0 = 0;
@@ -666,13 +708,13 @@ __device__ __forceinline__ bool stage_wait(uint64_t* bar, uint32_t parity, Strea
 }
 
 // A: PrefArgs (STREAM_STATS, STREAM_GRAD) or PolicyArgs; W likewise.
-template <class T, int kMode, class A, class W>
-__global__ void __launch_bounds__(kStreamThreads, 2) stream_kernel(A a, W w) {
+template <class T, int kMode, int kStages, int kBlocks, class A, class W>
+__global__ void __launch_bounds__(kStreamThreads, kBlocks) stream_kernel(A a, W w) {
   constexpr int kV = Row<T>::kV;
   extern __shared__ __align__(16) uint8_t ring[];
   Granule* stages = reinterpret_cast<Granule*>(ring);
-  StreamShared* sh =
-      reinterpret_cast<StreamShared*>(ring + (size_t)kStages * kStageGranules * 16);
+  auto* sh = reinterpret_cast<StreamShared<kStages>*>(ring +
+                                                      (size_t)kStages * kStageGranules * 16);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -941,27 +983,43 @@ unsigned blocks_for(int64_t items, int64_t most) {
   return (unsigned)(items < 1 ? 1 : items < most ? items : most);
 }
 
-template <class T, int kMode, class A, class W>
-cudaError_t launch_stream(const A& a, const W& w, Ctx& c) {
-  const auto fn = stream_kernel<T, kMode, A, W>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kStreamSmem);
+template <class T>
+bool row_per_warp(const Mat& x, const Ctx& c) {
+  return x.cols * (int64_t)sizeof(T) <=
+         (x.rows >= kRowsPerSm * c.num_sms ? kWarpBytes : kFewWarpBytes);
+}
+
+template <class T, int kMode, int kStages, int kBlocks, class A, class W>
+cudaError_t launch_ring(const A& a, const W& w, Ctx& c) {
+  const auto fn = stream_kernel<T, kMode, kStages, kBlocks, A, W>;
+  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)kStreamSmem<kStages>);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  cfg.gridDim = dim3(blocks_for(a.logits.rows, 2 * c.num_sms));
+  cfg.gridDim = dim3(blocks_for(a.logits.rows, kBlocks * c.num_sms));
   cfg.blockDim = dim3(kStreamThreads);
-  cfg.dynamicSmemBytes = kStreamSmem;
+  cfg.dynamicSmemBytes = kStreamSmem<kStages>;
   cfg.stream = c.stream;
   add_pdl_attr(c, cfg, attr);
   ++c.launches;
   return cudaLaunchKernelEx(&cfg, fn, a, w);
 }
 
+// Three blocks per SM with four stages, so that two work while one meets at the end of its
+// row, or two with six, which hold fewer rows in L2 between their reads (policy, 8192 x
+// 32,000 BF16: 185 us against 202; 4096 x 128,000: 430 against 389).
+constexpr int64_t kLongRow = 128 * 1024;
+template <class T, int kMode, class A, class W>
+cudaError_t launch_stream(const A& a, const W& w, Ctx& c) {
+  return a.logits.cols * (int64_t)sizeof(T) <= kLongRow ? launch_ring<T, kMode, 4, 3>(a, w, c)
+                                                        : launch_ring<T, kMode, 6, 2>(a, w, c);
+}
+
 template <class T>
 cudaError_t pref_typed(const PrefArgs& p, const PrefWs& w, Ctx& c) {
   const int64_t rows = p.logits.rows;
-  const bool warps = p.logits.cols <= kWarpCols;
+  const bool warps = row_per_warp<T>(p.logits, c);
   const unsigned blocks = (unsigned)((rows + kWarps - 1) / kWarps);
   cudaError_t e = cudaSuccess;
   if (rows)
@@ -976,7 +1034,7 @@ cudaError_t pref_typed(const PrefArgs& p, const PrefWs& w, Ctx& c) {
 
 template <class T>
 cudaError_t policy_typed(const PolicyArgs& p, const PolicyWs& w, Ctx& c) {
-  if (p.logits.cols > kWarpCols) return launch_stream<T, STREAM_POLICY>(p, w, c);
+  if (!row_per_warp<T>(p.logits, c)) return launch_stream<T, STREAM_POLICY>(p, w, c);
   return launch(c, blocks_for((p.logits.rows + kWarps - 1) / kWarps, 3 * c.num_sms), kBlock,
                 policy_warp_kernel<T>, p, w);
 }
