@@ -304,14 +304,41 @@ __device__ __forceinline__ MaxSum warp_max_sum(const Row<T>& r, int lane, float 
   return join_lanes<32>(acc, scale);
 }
 
-// The target's log probability, at most 0 (rounding may leave it above).  A finite logit
-// whose scaled distance to the maximum overflows: in natural units first.
-__device__ __forceinline__ float log_prob(float xt, MaxSum r, float scale) {
-  constexpr float kLn2 = 0.6931471805599453f;
-  const float t = exponent(xt, r.m, scale);
-  const bool out = t == -INFINITY && xt > -INFINITY;
-  const float lp = (out ? (xt - r.m) * (scale * kLn2) : t * kLn2) - logf(r.s);
-  return lp > 0.0f ? 0.0f : lp;
+// The target's log probability, at most 0 (rounding may leave it above), as a sum of two
+// numbers: what the losses take from it is its small difference to another one, and its
+// own rounding, 5e-7 at -10, would be most of their error.
+//   x * scale - base - log2 s = (x * scale - base - e) - log2 f,  s = 2^e f, f about 1
+// Where that leaves FP32 (infinities, NaN, a scaled maximum or distance out of range), in
+// one, a distance out of range in natural units first.
+struct Two {
+  float hi, lo;
+};
+__device__ __forceinline__ Two two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), v = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, v)), __fsub_rn(b, v))};
+}
+__device__ __forceinline__ Two log_prob(float xt, MaxSum r, float scale) {
+  constexpr float kLn2 = 0.693147182f, kLn2Rest = -1.90465430e-9f;  // (their sum is ln 2)
+  const float base = __fmul_rn(r.m, scale), p = __fmul_rn(xt, scale);
+  if (!(fabsf(base) < 1e30f && fabsf(p) < 1e30f && r.s > 1e-30f && r.s < 1e30f)) {
+    const float t = exponent(xt, r.m, scale);
+    const bool out = t == -INFINITY && xt > -INFINITY;
+    const float lp = (out ? (xt - r.m) * (scale * kLn2) : t * kLn2) - logf(r.s);
+    return {lp > 0.0f ? 0.0f : lp, 0.0f};
+  }
+  const uint32_t bits = __float_as_uint(r.s);
+  float e = (float)((int)(bits >> 23) - 127);
+  float f = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
+  if (f > 1.41421354f) {
+    f *= 0.5f;
+    e += 1.0f;
+  }
+  const Two d = two_sum(p, -base), u = two_sum(d.hi, -e);
+  const float rest = (d.lo + u.lo) + fmaf(xt, scale, -p);
+  const float q = __fmul_rn(u.hi, kLn2);
+  const float qr = fmaf(u.hi, kLn2, -q) + fmaf(u.hi, kLn2Rest, rest * kLn2);
+  const Two v = two_sum(q, -logf(f)), lp = two_sum(v.hi, v.lo + qr);
+  return lp.hi > 0.0f ? Two{0.0f, 0.0f} : lp;
 }
 // g * (1 - softmax) at the target
 __device__ __forceinline__ float target_grad(float g, float xt, MaxSum r, float scale) {
@@ -356,7 +383,7 @@ PrefLayout pref_layout(int64_t rows, int64_t pairs) {
   auto take = [&](size_t& f, size_t bytes) { f = o; o += align_up(bytes); };
   take(L.off_m, rows * 4);
   take(L.off_s, rows * 4);
-  take(L.off_lp, rows * 4);
+  take(L.off_lp, rows * 8);
   take(L.off_coef, rows * 4);
   take(L.off_loss, pairs * 8);
   L.total = o;
@@ -364,8 +391,8 @@ PrefLayout pref_layout(int64_t rows, int64_t pairs) {
 }
 struct PrefWs {
   Ctrl* ctrl;
-  float *m, *s, *lp, *coef;
-  double* loss;
+  float *m, *s, *coef;
+  double *lp, *loss;
 };
 
 constexpr int kBlock = 256;
@@ -374,10 +401,10 @@ constexpr int kBlock = 256;
 // barriers cost more than a warp's longer loop there.
 constexpr int64_t kWarpBytes = 16384, kFewWarpBytes = 4096, kRowsPerSm = 8;
 
-__device__ __forceinline__ void put_stats(const PrefWs& w, int64_t t, MaxSum r, float lp) {
+__device__ __forceinline__ void put_stats(const PrefWs& w, int64_t t, MaxSum r, Two lp) {
   w.m[t] = r.m;
   w.s[t] = r.s;
-  w.lp[t] = lp;
+  w.lp[t] = (double)lp.hi + (double)lp.lo;
   w.coef[t] = 0.0f;  // pref_pair_kernel sets that of the rows of a sequence
 }
 
@@ -391,7 +418,7 @@ __global__ void __launch_bounds__(kBlock, 3) pref_stats_warp_kernel(PrefArgs a, 
   const int64_t target = a.targets.at(t);
   const bool bad = target >= a.logits.cols;
   MaxSum r{0.0f, 0.0f};
-  float lp = 0.0f;
+  Two lp{0.0f, 0.0f};
   if (target >= 0 && !bad) {
     const Row<T> row(static_cast<const T*>(a.logits.p) + t * a.logits.ld, a.logits.cols);
     Held h;
@@ -519,6 +546,7 @@ constexpr int kMaxBlocks = 1024;
 struct PolicyWs {
   Ctrl* ctrl;
   double* part;  // per block: loss, KL term, weight of the clipped rows
+  float inv_t, scale;  // 1 and log2(e) over the temperature
 };
 
 // What the policy loss reads of a row beside its logits.
@@ -550,16 +578,17 @@ __device__ __forceinline__ RowLoss policy_row(const PolicyArgs& a, const RowInfo
                                               float inv_t, float scale) {
   RowLoss o{0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
   if (f.target < 0) return o;
-  o.lp = log_prob(f.xt, r, scale);
+  const Two lp = log_prob(f.xt, r, scale);
+  o.lp = lp.hi;
   if (f.weight == 0.0f) return o;
-  const float ratio = expf(o.lp - f.old_logp);
+  const float ratio = expf((lp.hi - f.old_logp) + lp.lo);
   const float held = fminf(fmaxf(ratio, 1.0f - a.clip_low), 1.0f + a.clip_high);
   const bool outside = f.adv >= 0.0f ? ratio > 1.0f + a.clip_high : ratio < 1.0f - a.clip_low;
   // (minimum and maximum drop a NaN: a ratio that is one stays one)
   float l = ratio == ratio ? -fminf(ratio * f.adv, held * f.adv) : ratio;
   float d = outside ? 0.0f : -ratio * f.adv;
   if (a.ref_logp) {
-    const float away = f.ref_logp - o.lp, em = expm1f(away);
+    const float away = (f.ref_logp - lp.hi) - lp.lo, em = expm1f(away);
     o.kl = f.weight * (em - away);
     l += a.kl * (em - away);
     d -= a.kl * em;
@@ -632,7 +661,7 @@ __global__ void __launch_bounds__(kBlock, 3) policy_warp_kernel(PolicyArgs a, Po
   wait_prior_grid();
   allow_next_grid();
   const int lane = threadIdx.x & 31;
-  const float inv_t = 1.0f / a.temperature, scale = kLog2e * inv_t;
+  const float inv_t = w.inv_t, scale = w.scale;
   PolicySums sums;
   for (int64_t t = ((int64_t)blockIdx.x * kBlock + threadIdx.x) >> 5; t < a.logits.rows;
        t += (int64_t)gridDim.x * (kBlock / 32)) {
@@ -729,9 +758,11 @@ __global__ void __launch_bounds__(kStreamThreads, kBlocks) stream_kernel(A a, W 
   allow_next_grid();
   const int64_t rows = a.logits.rows;
   const T* logits = static_cast<const T*>(a.logits.p);
-  float inv_t = 1.0f;
-  if constexpr (kMode == STREAM_POLICY) inv_t = 1.0f / a.temperature;
-  const float scale = kLog2e * inv_t;
+  float inv_t = 1.0f, scale = kLog2e;
+  if constexpr (kMode == STREAM_POLICY) {
+    inv_t = w.inv_t;
+    scale = w.scale;
+  }
   const bool write = kMode != STREAM_STATS && a.grad.p;
   // the i-th row of the block (the gradient's pass goes through the rows backwards)
   auto row_at = [&](int64_t i) {
@@ -902,7 +933,7 @@ __global__ void __launch_bounds__(kStreamThreads, kBlocks) stream_kernel(A a, W 
           }
         } else if (lane == 0) {
           put_stats(w, t, read ? r : MaxSum{0.0f, 0.0f},
-                    read ? log_prob(f.xt, r, scale) : 0.0f);
+                    read ? log_prob(f.xt, r, scale) : Two{0.0f, 0.0f});
         }
       }
       meet();
@@ -1053,8 +1084,8 @@ cudaError_t launch_preference(const PrefArgs& p, void* ws, Ctx& c) {
   const PrefLayout L = pref_layout(p.logits.rows, p.pairs);
   char* b = static_cast<char*>(ws);
   auto f = [&](size_t o) { return reinterpret_cast<float*>(b + o); };
-  const PrefWs w{reinterpret_cast<Ctrl*>(b), f(L.off_m), f(L.off_s), f(L.off_lp), f(L.off_coef),
-                 reinterpret_cast<double*>(b + L.off_loss)};
+  const PrefWs w{reinterpret_cast<Ctrl*>(b), f(L.off_m), f(L.off_s), f(L.off_coef),
+                 reinterpret_cast<double*>(b + L.off_lp), reinterpret_cast<double*>(b + L.off_loss)};
   if (p.logits.dtype == CASGD_F32) return pref_typed<float>(p, w, c);
   if (p.logits.dtype == CASGD_BF16) return pref_typed<__nv_bfloat16>(p, w, c);
   return pref_typed<__half>(p, w, c);
@@ -1062,7 +1093,8 @@ cudaError_t launch_preference(const PrefArgs& p, void* ws, Ctx& c) {
 
 cudaError_t launch_policy(const PolicyArgs& p, void* ws, Ctx& c) {
   char* b = static_cast<char*>(ws) + align_up(sizeof(Ctrl));
-  const PolicyWs w{static_cast<Ctrl*>(ws), reinterpret_cast<double*>(b)};
+  const PolicyWs w{static_cast<Ctrl*>(ws), reinterpret_cast<double*>(b), 1.0f / p.temperature,
+                   (float)(1.4426950408889634 / (double)p.temperature)};
   if (p.logits.dtype == CASGD_F32) return policy_typed<float>(p, w, c);
   if (p.logits.dtype == CASGD_BF16) return policy_typed<__nv_bfloat16>(p, w, c);
   return policy_typed<__half>(p, w, c);
