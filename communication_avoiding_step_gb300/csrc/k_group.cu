@@ -18,9 +18,10 @@
 // 256 x 256 x 64 products, two thirds of what one CTA needs for a 128 x 256 tile of its own.
 // What bounds it: the copies into shared memory take as long as the products (8192^3: 459 us
 // alone, the products alone 484, together 593), and a ring of 192 KB per SM has to cover
-// their latency.  Measured, BF16: 8192^3 1.85 PFLOP/s (dW 1.77); 16384 rows of 32 ragged experts,
-// 2048 x 2816: Y 124 us, dX 123, dW 158 (99, 102 and 130 without the loads); one 128 x 256
-// tile per CTA took 180 (Y) and 220 us (dW).
+// their latency.  Measured, BF16: 8192^3 1.85 to 1.93 PFLOP/s (570 to 594 us); 16384 rows
+// of 32 ragged experts, 2048 x 2816, Y 124 us, dX 123, dW 158 with the same inputs over and
+// over (99, 102 and 130 without the loads), Y 142 and dW 165 with others each time; one
+// 128 x 256 tile per CTA took 180 (Y) and 220 us (dW).
 //
 // The copying and the MMA warp run their loops whole, so that the values their instructions
 // take are uniform, and one lane issues (one lane in the loop: 139 us instead of 124).
@@ -44,8 +45,8 @@
 // takes as MN-major operands, so nothing is transposed in memory.
 //
 // TMA needs rows on 16-byte boundaries.  Inputs without them (odd widths or pitches) are
-// copied once into the workspace with padded rows; outputs without them are stored element
-// by element.
+// copied into the workspace with padded rows by each call; outputs without them are stored
+// 32 elements of a row at a time (4452 rows, 64 experts, 1649 x 419: 70 us in all).
 #include <atomic>
 #include <cstring>
 
@@ -64,6 +65,7 @@ constexpr int kStageBytes = 2 * kHalf;
 constexpr int kMaxGroups = CASGD_MAX_GROUPS;
 constexpr uint64_t kTimeoutNs = 1000000000ull;
 constexpr uint32_t kTmemCols = 2 * BN;
+// (dX of 14,876 rows, one expert, 2328 x 3688: 194 us, in whole rows of tiles 238.)
 constexpr int kPanel = 8;
 // Eight epilogue warps, two per quarter of TMEM's lanes: with four, the short tiles of dW
 // (and stores of Y and dX) waited for their epilogue.
